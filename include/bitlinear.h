@@ -305,6 +305,181 @@ bl_status bl_bitlinear_backward_w(const uint16_t* dy, const int8_t* xq, const fl
  * Errors: BL_ERR_NULL, BL_ERR_SHAPE, BL_ERR_ALIGN, BL_ERR_HIP. */
 bl_status bl_unpack_ternary(const uint8_t* packed, int64_t n, int64_t k, int8_t* q, void* stream);
 
+/* ---- Around the BitLinear layers of a transformer block ----
+ * [P2, P3]: the 2B4T block keeps norms, rotary positions and attention around
+ * its ternary layers.  The calls below take and give what those layers give
+ * and take: bf16 activations, int8 rows with their absmax, fp32 gradients. */
+
+/* Root-mean-square norm of each row, with the residual's addition before it
+ * and the int8 quantization that bl_linear expects after it:
+ *   h = x + residual (fp32; h = x without one),   r = bf16(h),
+ *   n = (h * w) * c,  c = 1 / sqrt(mean_j h_j^2 + eps)       (fp32),
+ *   alpha = max_j |n_j|,  s = fl32(127 / max(alpha, 1e-5f)),
+ *   xq = round_half_even(fl32(n * s)),
+ *   y = bf16(n),   xhat = bf16(xq * fl32(alpha / 127)).
+ * The norm and its codes are those of the fp32 sum, not of the rounded r.
+ *   x, residual  [m][k] bf16; residual may be NULL.
+ *   weight       [k] fp32.   eps finite, >= 0.
+ *   r, y, xhat   out [m][k] bf16, each NULL to skip it; r may be x or residual.
+ *   xq, alpha    out [m][k] int8 and [m] fp32, both or neither NULL.
+ * At least one output is required.  k is a multiple of 64, at most
+ * BL_MAX_NORM_K (a row stays in registers); |h| below 2^56, so that the sum of
+ * squares is finite.  x, residual, weight and the [m][k] outputs are 16-byte
+ * aligned.
+ * Errors: BL_ERR_NULL, BL_ERR_SHAPE (also a bad eps), BL_ERR_ALIGN, BL_ERR_HIP. */
+#define BL_MAX_NORM_K 32768
+bl_status bl_rmsnorm_quant(const uint16_t* x, const uint16_t* residual, const float* weight, int64_t m, int64_t k,
+                           float eps, uint16_t* r, uint16_t* y, uint16_t* xhat, int8_t* xq, float* alpha,
+                           void* stream);
+
+/* Device workspace of bl_rmsnorm_backward: partial sums of dw.  Returns 0 for
+ * an invalid shape. */
+size_t bl_rmsnorm_backward_workspace_bytes(int64_t m, int64_t k);
+
+/* Gradients of the norm (the quantizer is the identity in the backward pass,
+ * as for bl_bitlinear_backward_x, whose fp32 dx is the dn here):
+ *   c = 1 / sqrt(mean_j r_j^2 + eps),
+ *   dx = bf16(c * (dn * w - r * c^2 * mean_j(dn_j w_j r_j)) + dr),
+ *   dw = sum_i dn_i * r_i * c_i                               (fp32 sums).
+ *   dn      [m][k] fp32; r [m][k] bf16, the norm's input as stored (r of the
+ *           forward call, or x without a residual).
+ *   dr      [m][k] bf16, the gradient that reaches r past the norm, or NULL.
+ *   dx      out [m][k] bf16: the gradient of x and of the residual alike; may be dr.
+ *   dw      out [k] fp32 (overwritten; zero for m = 0).
+ * The order of the sums is fixed: equal inputs give equal bits.
+ * Errors: BL_ERR_NULL, BL_ERR_SHAPE, BL_ERR_ALIGN, BL_ERR_WORKSPACE, BL_ERR_HIP. */
+bl_status bl_rmsnorm_backward(const float* dn, const uint16_t* r, const float* weight, const uint16_t* dr, int64_t m,
+                              int64_t k, float eps, uint16_t* dx, float* dw, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* Rotary positions.  Pair i of a head (i < rot / 2) turns by the angle
+ * position * f_i:
+ *   (a, b) -> magnitude * (a cos - b sin, a sin + b cos),
+ * a and b being elements i and i + rot/2 (interleaved = 0) or 2i and 2i + 1
+ * (interleaved = 1); elements from rot on pass unchanged.  f_i is held as
+ * turns per position in two fp32 numbers (value and remainder), with which the
+ * fraction of a turn is right to about 2^-23 for positions below 2^24. */
+typedef struct bl_rope_table {
+    const float* turns; /* device, [rot / 2][2] fp32, as bl_rope_frequencies fills it */
+    int64_t rot;        /* even, 0 < rot <= head dimension                           */
+    int32_t interleaved;
+    float magnitude; /* multiplies both outputs (1 unless a long-context scaling asks for more) */
+} bl_rope_table;
+
+/* Table of frequencies (host memory, evaluated in 64 bits):
+ *   f_i = base^(-2i / rot), then
+ *   BL_ROPE_PLAIN   as it is;
+ *   BL_ROPE_LINEAR  f_i / factor (positions interpolated);
+ *   BL_ROPE_BASE    base * factor^(rot / (rot - 2)) in base's place (the slowest
+ *                   pair is slowed by factor, the fastest not at all; rot > 2);
+ *   BL_ROPE_BLEND   with t = original * f_i / 2 pi turns over the original
+ *                   length: f_i where t >= fast, f_i / factor where t <= slow,
+ *                   and in between the two weighted linearly in t.
+ * turns: [rot / 2][2] floats.  Errors: BL_ERR_NULL, BL_ERR_SHAPE (rot odd or
+ * not in 2..BL_MAX_HEAD_DIM, a value that is not positive and finite, slow >= fast). */
+enum { BL_ROPE_PLAIN = 0, BL_ROPE_LINEAR = 1, BL_ROPE_BASE = 2, BL_ROPE_BLEND = 3 };
+#define BL_MAX_HEAD_DIM 256
+bl_status bl_rope_frequencies(int64_t rot, double base, int scaling, double factor, double original, double fast,
+                              double slow, float* turns);
+
+/* Rotates the heads of every token.
+ *   x, y       [tokens][heads][dim] bf16 with strides in elements (multiples of
+ *              8; the dim elements of a head are adjacent); y may be x.
+ *   position   [tokens] int32 (device).
+ *   inverse    non-zero: the transposed rotation, the gradient of the forward
+ *              one (the same magnitude).
+ * dim: a multiple of 8, at most BL_MAX_HEAD_DIM.
+ * Errors: BL_ERR_NULL, BL_ERR_SHAPE, BL_ERR_ALIGN (also strides), BL_ERR_HIP. */
+bl_status bl_rope(const uint16_t* x, int64_t x_token_stride, int64_t x_head_stride, const int32_t* position,
+                  const bl_rope_table* rope, int64_t tokens, int64_t heads, int64_t dim, int inverse, uint16_t* y,
+                  int64_t y_token_stride, int64_t y_head_stride, void* stream);
+
+/* A key/value cache in 8 bits.  A page holds page_tokens consecutive tokens of
+ * one sequence; k and v are int8 [pages][heads][page_tokens][dim], k_absmax
+ * and v_absmax fp32 [pages][heads]: a code q of a page and head stands for
+ * q * absmax / 127.  page_tokens: 16, 32, 64, 128 or 256; dim: a multiple of
+ * 16, at most BL_MAX_HEAD_DIM; k and v are 16-byte aligned.  Positions may
+ * address more than 2^32 bytes. */
+typedef struct bl_kv_cache {
+    int8_t* k;
+    int8_t* v;
+    float* k_absmax;
+    float* v_absmax;
+    int64_t pages;
+    int32_t heads;
+    int32_t page_tokens;
+    int32_t dim;
+} bl_kv_cache;
+
+/* The tokens of one step: tokens offsets[s] .. offsets[s + 1] - 1 belong to
+ * sequence s and stand at positions start[s], start[s] + 1, ...; position p of
+ * sequence s is token p % page_tokens of page page_table[s][p / page_tokens].
+ * max_new and max_len bound offsets[s + 1] - offsets[s] and start[s] +
+ * offsets[s + 1] - offsets[s]; max_len <= table_stride * page_tokens.  A page
+ * number outside 0 .. pages - 1 marks a page that is not there: nothing is
+ * written to it, reading it gives zeros, attention skips it. */
+typedef struct bl_kv_batch {
+    const int32_t* page_table; /* device [seqs][table_stride] */
+    const int32_t* start;      /* device [seqs], >= 0         */
+    const int32_t* offsets;    /* device [seqs + 1], ascending from 0 to tokens */
+    int64_t seqs;
+    int64_t table_stride;
+    int64_t tokens;
+    int64_t max_new;
+    int64_t max_len;
+} bl_kv_batch;
+
+/* Writes the step's keys and values into the cache, quantized on the way.
+ * For each page and head that new tokens enter, with a_old its absmax if it
+ * holds earlier tokens of the sequence (else 0):
+ *   a = max(a_old, max |new values|),  codes of new values
+ *   round_half_even(fl32(value * fl32(127 / a))), and, where a > a_old, those
+ *   already there become round_half_even(fl32(q * fl32(a_old / a)));
+ * pages whose values all stay below 2^-64 are written as zeros with absmax 0.
+ * Writing the same tokens again gives the same cache.  A page that is written
+ * must belong to one sequence of the batch only.
+ *   k, v   bf16 [tokens][heads][dim], strides in elements (multiples of 8).
+ *   rope   NULL, or the rotation that keys take at their positions before they
+ *          are quantized (in fp32, without a rounding to bf16 in between).
+ *   q      with rope: bf16 [tokens][q_heads][dim], rotated alike into q_out
+ *          [tokens][q_heads][dim] bf16 (contiguous; q_out may be q if q is
+ *          contiguous too); or NULL.
+ * Errors: BL_ERR_NULL, BL_ERR_SHAPE, BL_ERR_ALIGN, BL_ERR_HIP. */
+bl_status bl_kv_append(const bl_kv_cache* cache, const bl_kv_batch* batch, const uint16_t* k, int64_t k_token_stride,
+                       int64_t k_head_stride, const uint16_t* v, int64_t v_token_stride, int64_t v_head_stride,
+                       const bl_rope_table* rope, const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
+                       int64_t q_heads, uint16_t* q_out, void* stream);
+
+/* Reads the batch's tokens back: bf16(q * fl32(absmax / 127)), zeros where the
+ * page is not there.   k, v  out bf16 [tokens][heads][dim], contiguous.
+ * Errors: BL_ERR_NULL, BL_ERR_SHAPE, BL_ERR_ALIGN, BL_ERR_HIP. */
+bl_status bl_kv_read(const bl_kv_cache* cache, const bl_kv_batch* batch, uint16_t* k, uint16_t* v, void* stream);
+
+/* Device workspace of bl_attention (0: none is needed, or an argument is invalid). */
+size_t bl_attention_workspace_bytes(const bl_kv_cache* cache, const bl_kv_batch* batch, int64_t q_heads);
+
+/* Attention of the step's queries over the cache, which already holds the
+ * step's own tokens (bl_kv_append):
+ *   out = sum_j p_j v_j,  p = softmax_j(scale * q . k_j)
+ * over the positions j <= p of its sequence, p being the query's own; with
+ * window > 0 only those with p - j < window or j < sinks.  Query head h reads
+ * cache head h / (q_heads / heads).  A query that sees nothing (its pages are
+ * not there) gives zeros.
+ *   q      bf16 [tokens][q_heads][dim], strides in elements (multiples of 8).
+ *   out    bf16 [tokens][q_heads][dim], contiguous.
+ *   lse    NULL, or out fp32 [tokens][q_heads]: log sum_j exp(scale * q . k_j)
+ *          (-inf for a query that sees nothing).
+ * Keys are read as stored; a query row enters the products as 16-bit integers
+ * relative to its absmax; softmax statistics and sums are fp32; the weights
+ * enter the product with v in fp16, scaled so that none above 2^-28 of the
+ * row's largest contribution loses precision.  The result does not depend on
+ * the order in which workgroups run.
+ * Errors: BL_ERR_NULL, BL_ERR_SHAPE (also q_heads no multiple of heads, sinks
+ * without a window, scale not finite), BL_ERR_ALIGN, BL_ERR_WORKSPACE, BL_ERR_HIP. */
+bl_status bl_attention(const bl_kv_cache* cache, const bl_kv_batch* batch, const uint16_t* q, int64_t q_token_stride,
+                       int64_t q_head_stride, int64_t q_heads, float scale, int64_t window, int64_t sinks,
+                       uint16_t* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* bl_status_string(bl_status s);
 

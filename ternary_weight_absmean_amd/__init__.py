@@ -24,6 +24,8 @@ __all__ = [
     "bl_ternarize_pack_glu", "bl_linear_glu", "bl_bitlinear_glu", "bl_pack_transposed", "bl_bitlinear_backward_x",
     "bl_backward_w_workspace_bytes", "bl_bitlinear_backward_w", "bl_ternarize_pack_noalloc",
     "bl_packed_bytes_b3", "bl_ternarize_pack_b3", "bl_bitlinear_b3",
+    "bl_rmsnorm_quant", "bl_rmsnorm_backward_workspace_bytes", "bl_rmsnorm_backward", "bl_rope_frequencies", "bl_rope",
+    "Rope", "KVCache", "KVBatch", "bl_kv_append", "bl_kv_read", "bl_attention_workspace_bytes", "bl_attention",
 ]
 
 
@@ -79,6 +81,25 @@ _lib.bl_backward_w_workspace_bytes.restype = _SZ
 _lib.bl_bitlinear_backward_w.argtypes = [_P, _P, _P, _I64, _I64, _I64, _P, _P, _SZ, _P]
 _lib.bl_bitlinear_backward_w.restype = ctypes.c_int
 _lib.bl_unpack_ternary.restype = ctypes.c_int
+_F32, _F64, _INT = ctypes.c_float, ctypes.c_double, ctypes.c_int
+_lib.bl_rmsnorm_quant.argtypes = [_P, _P, _P, _I64, _I64, _F32, _P, _P, _P, _P, _P, _P]
+_lib.bl_rmsnorm_quant.restype = _INT
+_lib.bl_rmsnorm_backward_workspace_bytes.argtypes = [_I64, _I64]
+_lib.bl_rmsnorm_backward_workspace_bytes.restype = _SZ
+_lib.bl_rmsnorm_backward.argtypes = [_P, _P, _P, _P, _I64, _I64, _F32, _P, _P, _P, _SZ, _P]
+_lib.bl_rmsnorm_backward.restype = _INT
+_lib.bl_rope_frequencies.argtypes = [_I64, _F64, _INT, _F64, _F64, _F64, _F64, _P]
+_lib.bl_rope_frequencies.restype = _INT
+_lib.bl_rope.argtypes = [_P, _I64, _I64, _P, _P, _I64, _I64, _I64, _INT, _P, _I64, _I64, _P]
+_lib.bl_rope.restype = _INT
+_lib.bl_kv_append.argtypes = [_P, _P, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _I64, _P, _P]
+_lib.bl_kv_append.restype = _INT
+_lib.bl_kv_read.argtypes = [_P, _P, _P, _P, _P]
+_lib.bl_kv_read.restype = _INT
+_lib.bl_attention_workspace_bytes.argtypes = [_P, _P, _I64]
+_lib.bl_attention_workspace_bytes.restype = _SZ
+_lib.bl_attention.argtypes = [_P, _P, _P, _I64, _I64, _I64, _F32, _I64, _I64, _P, _P, _P, _SZ, _P]
+_lib.bl_attention.restype = _INT
 _lib.bl_status_string.argtypes = [ctypes.c_int]
 _lib.bl_status_string.restype = ctypes.c_char_p
 
@@ -410,3 +431,241 @@ def bl_unpack_ternary(packed: torch.Tensor, n: int, k: int, q: torch.Tensor | No
         q = torch.empty((n, k), dtype=torch.int8, device=packed.device)
     _check("bl_unpack_ternary", _lib.bl_unpack_ternary(_ptr(packed), n, k, _ptr(q), _stream(packed.device)))
     return q
+
+
+# ---- around the BitLinear layers ----
+
+def _dense(t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple) -> int | None:
+    """Address of a dense device tensor of this type and shape (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        _need(t, name, dtype, shape)
+    return t.data_ptr()
+
+
+def _heads(t: torch.Tensor, name: str, shape: tuple) -> tuple[int, int, int]:
+    """Address and (token, head) strides of bf16 ``[tokens][heads][dim]`` whose last axis is adjacent."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    token, head, one = t.stride()
+    if one != 1 and shape[2] > 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    return t.data_ptr(), token, head
+
+
+def bl_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: torch.Tensor | None = None,
+                     r: torch.Tensor | None | bool = None, y: torch.Tensor | None | bool = None,
+                     xhat: torch.Tensor | None | bool = None, xq: torch.Tensor | None | bool = True,
+                     alpha: torch.Tensor | None = None):
+    """RMS norm of ``x + residual`` (bf16 ``[m][k]``) with int8 output for bl_linear:
+    returns (xq, alpha, r, y, xhat), None where an output is not asked for.
+
+    ``r`` (the bf16 sum), ``y`` (the bf16 norm), ``xhat`` (bf16 of what the codes stand for), ``xq``: a tensor to
+    write into, True to allocate, or False/None to skip; ``r`` is allocated by default if there is a residual."""
+    _need(x, "x", torch.bfloat16)
+    shape = m, k = x.shape
+    dev = x.device
+    if r is None:
+        r = residual is not None
+    r, y, xhat = (torch.empty_like(x) if t is True else t if isinstance(t, torch.Tensor) else None for t in (r, y, xhat))
+    if xq is True:
+        xq = torch.empty(shape, dtype=torch.int8, device=dev)
+    xq = xq if isinstance(xq, torch.Tensor) else None
+    if xq is None:
+        alpha = None
+    elif alpha is None:
+        alpha = torch.empty(m, dtype=torch.float32, device=dev)
+    _check("bl_rmsnorm_quant", _lib.bl_rmsnorm_quant(
+        x.data_ptr(), _dense(residual, "residual", torch.bfloat16, shape), _dense(weight, "weight", torch.float32, (k,)),
+        m, k, eps, _dense(r, "r", torch.bfloat16, shape), _dense(y, "y", torch.bfloat16, shape),
+        _dense(xhat, "xhat", torch.bfloat16, shape), _dense(xq, "xq", torch.int8, shape),
+        _dense(alpha, "alpha", torch.float32, (m,)), _stream(dev)))
+    return xq, alpha, r, y, xhat
+
+
+def bl_rmsnorm_backward_workspace_bytes(m: int, k: int) -> int:
+    return int(_lib.bl_rmsnorm_backward_workspace_bytes(m, k))
+
+
+def bl_rmsnorm_backward(dn: torch.Tensor, r: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
+                        dr: torch.Tensor | None = None, dx: torch.Tensor | None = None, dw: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None):
+    """Gradients of bl_rmsnorm_quant: fp32 ``dn`` (of the norm's output) and bf16 ``dr`` (of the sum, past the
+    norm; optional) -> (dx bf16 [m][k], dw fp32 [k])."""
+    _need(dn, "dn", torch.float32)
+    shape = m, k = dn.shape
+    dev = dn.device
+    if dx is None:
+        dx = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    if dw is None:
+        dw = torch.empty(k, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(max(bl_rmsnorm_backward_workspace_bytes(m, k), 16), dtype=torch.uint8, device=dev)
+    _check("bl_rmsnorm_backward", _lib.bl_rmsnorm_backward(
+        dn.data_ptr(), _dense(r, "r", torch.bfloat16, shape), _dense(weight, "weight", torch.float32, (k,)),
+        _dense(dr, "dr", torch.bfloat16, shape), m, k, eps, _dense(dx, "dx", torch.bfloat16, shape),
+        _dense(dw, "dw", torch.float32, (k,)), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream(dev)))
+    return dx, dw
+
+
+_ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "blend": 3}
+
+
+def bl_rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                        original: float = 0.0, fast: float = 32.0, slow: float = 1.0) -> torch.Tensor:
+    """Table of rotary frequencies, fp32 ``[rot / 2][2]`` on the host; ``scaling`` is "plain", "linear", "base" or
+    "blend" (BL_ROPE_* of the header; ``original``, ``fast`` and ``slow`` belong to "blend")."""
+    turns = torch.empty((max(rot // 2, 1), 2), dtype=torch.float32)
+    _check("bl_rope_frequencies", _lib.bl_rope_frequencies(rot, base, _ROPE_SCALINGS[scaling], factor, original, fast,
+                                                           slow, turns.data_ptr()))
+    return turns
+
+
+class Rope:
+    """Rotary positions: a frequency table on the device (``bl_rope_frequencies(...).to(device)``, fp32
+    ``[rot / 2][2]``), the layout of pairs and a magnitude that multiplies the result."""
+
+    class _Struct(ctypes.Structure):
+        _fields_ = [("turns", _P), ("rot", _I64), ("interleaved", ctypes.c_int32), ("magnitude", _F32)]
+
+    def __init__(self, turns: torch.Tensor, interleaved: bool = False, magnitude: float = 1.0):
+        _need(turns, "turns", torch.float32)
+        if turns.dim() != 2 or turns.shape[1] != 2:
+            raise ValueError(f"turns must have shape (rot / 2, 2), got {tuple(turns.shape)}")
+        self.turns = turns
+        self.struct = Rope._Struct(turns.data_ptr(), 2 * turns.shape[0], int(interleaved), magnitude)
+        self.address = ctypes.addressof(self.struct)
+
+
+def bl_rope(x: torch.Tensor, position: torch.Tensor, rope: Rope, inverse: bool = False,
+            out: torch.Tensor | None = None) -> torch.Tensor:
+    """bf16 heads ``[tokens][heads][dim]`` (the last axis adjacent) rotated by their int32 positions ``[tokens]``;
+    ``inverse`` gives the gradient's direction; ``out`` may be ``x``."""
+    tokens, heads, dim = shape = x.shape
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+    xp, xt, xh = _heads(x, "x", shape)
+    yp, yt, yh = _heads(out, "out", shape)
+    _check("bl_rope", _lib.bl_rope(xp, xt, xh, _dense(position, "position", torch.int32, (tokens,)), rope.address, tokens,
+                                   heads, dim, int(inverse), yp, yt, yh, _stream(x.device)))
+    return out
+
+
+class KVCache:
+    """Key/value cache in 8 bits: int8 ``k``, ``v`` [pages][heads][page_tokens][dim] and fp32 ``k_absmax``,
+    ``v_absmax`` [pages][heads].  Holds the tensors that it is given."""
+
+    class _Struct(ctypes.Structure):
+        _fields_ = [("k", _P), ("v", _P), ("k_absmax", _P), ("v_absmax", _P), ("pages", _I64),
+                    ("heads", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("dim", ctypes.c_int32)]
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_absmax: torch.Tensor, v_absmax: torch.Tensor):
+        _need(k, "k", torch.int8)
+        if k.dim() != 4:
+            raise ValueError(f"k must have shape (pages, heads, page_tokens, dim), got {tuple(k.shape)}")
+        _need(v, "v", torch.int8, k.shape)
+        _need(k_absmax, "k_absmax", torch.float32, k.shape[:2])
+        _need(v_absmax, "v_absmax", torch.float32, k.shape[:2])
+        self.k, self.v, self.k_absmax, self.v_absmax = k, v, k_absmax, v_absmax
+        self.pages, self.heads, self.page_tokens, self.dim = k.shape
+        self.struct = KVCache._Struct(k.data_ptr(), v.data_ptr(), k_absmax.data_ptr(), v_absmax.data_ptr(), *k.shape)
+        self.address = ctypes.addressof(self.struct)
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, page_tokens: int, dim: int, device) -> "KVCache":
+        """A cache of its own, zeroed."""
+        k = torch.zeros((pages, heads, page_tokens, dim), dtype=torch.int8, device=device)
+        a = torch.zeros((pages, heads), dtype=torch.float32, device=device)
+        return cls(k, torch.zeros_like(k), a, torch.zeros_like(a))
+
+
+class KVBatch:
+    """The tokens of one step: int32 device tensors ``page_table`` [seqs][stride], ``start`` [seqs] (tokens that
+    each sequence had before) and ``offsets`` [seqs + 1] (where its new tokens begin among the step's ``tokens``);
+    ``max_new`` and ``max_len`` bound a sequence's new tokens and its length with them."""
+
+    class _Struct(ctypes.Structure):
+        _fields_ = [("page_table", _P), ("start", _P), ("offsets", _P), ("seqs", _I64), ("table_stride", _I64),
+                    ("tokens", _I64), ("max_new", _I64), ("max_len", _I64)]
+
+    def __init__(self, page_table: torch.Tensor, start: torch.Tensor, offsets: torch.Tensor, tokens: int, max_new: int,
+                 max_len: int):
+        _need(page_table, "page_table", torch.int32)
+        if page_table.dim() != 2:
+            raise ValueError(f"page_table must have shape (seqs, stride), got {tuple(page_table.shape)}")
+        seqs, stride = page_table.shape
+        _need(start, "start", torch.int32, (seqs,))
+        _need(offsets, "offsets", torch.int32, (seqs + 1,))
+        self.page_table, self.start, self.offsets = page_table, start, offsets
+        self.tokens, self.max_new, self.max_len = int(tokens), int(max_new), int(max_len)
+        self.struct = KVBatch._Struct(page_table.data_ptr(), start.data_ptr(), offsets.data_ptr(), seqs, stride,
+                                      self.tokens, self.max_new, self.max_len)
+        self.address = ctypes.addressof(self.struct)
+
+
+def bl_kv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, rope: Rope | None = None,
+                 q: torch.Tensor | None = None, q_out: torch.Tensor | None = None) -> torch.Tensor | None:
+    """Writes the step's bf16 keys and values ``[tokens][heads][dim]`` into the cache, keys rotated on the way if
+    there is a ``rope``; with it, ``q`` [tokens][q_heads][dim] is rotated too and returned (dense)."""
+    shape = (batch.tokens, cache.heads, cache.dim)
+    kp, kt, kh = _heads(k, "k", shape)
+    vp, vt, vh = _heads(v, "v", shape)
+    qp = qt = qh = q_heads = out = None
+    if q is not None:
+        if rope is None:
+            raise ValueError("q is only rotated: it needs a rope")
+        q_heads = q.shape[1]
+        q_shape = (batch.tokens, q_heads, cache.dim)
+        qp, qt, qh = _heads(q, "q", q_shape)
+        if q_out is None:
+            q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=q.device)
+        out = _dense(q_out, "q_out", torch.bfloat16, q_shape)
+    _check("bl_kv_append", _lib.bl_kv_append(cache.address, batch.address, kp, kt, kh, vp, vt, vh,
+                                             rope.address if rope is not None else None, qp, qt or 0, qh or 0,
+                                             q_heads or 0, out, _stream(k.device)))
+    return q_out if q is not None else None
+
+
+def bl_kv_read(cache: KVCache, batch: KVBatch, k: torch.Tensor | None = None, v: torch.Tensor | None = None):
+    """The batch's tokens as the cache holds them: bf16 k, v ``[tokens][heads][dim]``."""
+    shape, dev = (batch.tokens, cache.heads, cache.dim), cache.k.device
+    if k is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    if v is None:
+        v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    _check("bl_kv_read", _lib.bl_kv_read(cache.address, batch.address, _dense(k, "k", torch.bfloat16, shape),
+                                         _dense(v, "v", torch.bfloat16, shape), _stream(dev)))
+    return k, v
+
+
+def bl_attention_workspace_bytes(cache: KVCache, batch: KVBatch, q_heads: int) -> int:
+    return int(_lib.bl_attention_workspace_bytes(cache.address, batch.address, q_heads))
+
+
+def bl_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, scale: float | None = None, window: int = 0,
+                 sinks: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of the step's bf16 queries ``[tokens][q_heads][dim]`` over the cache (which holds the step's own
+    tokens): bf16, dense.  ``scale`` is 1 / sqrt(dim) by default; ``window`` > 0 leaves the last ``window`` positions
+    and the first ``sinks`` visible; ``lse`` (fp32 [tokens][q_heads]) takes the logarithms of the softmax sums."""
+    q_heads = q.shape[1]
+    shape = (batch.tokens, q_heads, cache.dim)
+    qp, qt, qh = _heads(q, "q", shape)
+    if scale is None:
+        scale = cache.dim ** -0.5
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    if workspace is None:
+        nbytes = _lib.bl_attention_workspace_bytes(cache.address, batch.address, q_heads)
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+    _check("bl_attention", _lib.bl_attention(cache.address, batch.address, qp, qt, qh, q_heads, scale, window, sinks,
+                                             _dense(out, "out", torch.bfloat16, shape),
+                                             _dense(lse, "lse", torch.float32, shape[:2]), workspace.data_ptr(),
+                                             workspace.numel() * workspace.element_size(), _stream(q.device)))
+    return out

@@ -11,7 +11,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(HERE, "libbitlinear.so")
-SOURCES = ["abi.hip", "pack.hip", "quant.hip", "gemv.hip", "gemm.hip", "backward.hip", "b3.hip"]
+SOURCES = ["abi.hip", "pack.hip", "quant.hip", "gemv.hip", "gemm.hip", "backward.hip", "b3.hip", "norm.hip", "cache.hip",
+           "attention.hip"]
 MEASURE_LIB_PATH = os.path.join(HERE, "libblmeasure.so")
 MEASURE_SOURCES = ["measure.hip"]
 

@@ -91,4 +91,49 @@ bool gemv_fused_glu_applies(int64_t m, int64_t f, int64_t k);
 hipError_t launch_gemv_fused_glu(const uint8_t* packed, const float* gamma, const uint16_t* x, int64_t m, int64_t f,
                                  int64_t k, int8_t* xq, float* alpha, uint16_t* h, hipStream_t s);
 
+// RMS norm with residual and int8 output, and its gradients (k at most 32768).
+hipError_t launch_rmsnorm_quant(const uint16_t* x, const uint16_t* residual, const float* w, int64_t m, int64_t k,
+                                float eps, uint16_t* r, uint16_t* y, uint16_t* xhat, int8_t* xq, float* alpha,
+                                hipStream_t s);
+size_t rmsnorm_backward_workspace_bytes(int64_t m, int64_t k);
+hipError_t launch_rmsnorm_backward(const float* dn, const uint16_t* r, const float* w, const uint16_t* dr, int64_t m,
+                                   int64_t k, float eps, uint16_t* dx, float* dw, void* workspace, hipStream_t s);
+
+hipError_t launch_rope(const uint16_t* x, int64_t xt, int64_t xh, const int32_t* position, const float* turns, int rot,
+                       bool interleaved, float magnitude, int64_t tokens, int heads, int dim, bool inverse, uint16_t* y,
+                       int64_t yt, int64_t yh, hipStream_t s);
+
+// The 8-bit key/value cache as kernels see it.
+struct KvView {
+  int8_t *k, *v;               // [pages][heads][page_tokens][dim]
+  float *k_absmax, *v_absmax;  // [pages][heads]
+  int64_t pages;
+  int heads, page_tokens, dim;
+};
+
+// The tokens of a step.  What the host cannot see (device integers) is brought
+// into range here, so that no value of them leads outside a buffer.
+struct KvStep {
+  const int32_t *page_table, *start, *offsets;
+  int64_t table_stride;
+  int tokens, max_new;
+  __device__ int begin(int s) const { return min(max(offsets[s], 0), tokens); }
+  __device__ int count(int s, int begin) const { return min(min(max(offsets[s + 1], begin), tokens) - begin, max_new); }
+  __device__ int start_of(int s) const { return min(max(start[s], 0), 1 << 29); }
+  __device__ int64_t page(int s, int64_t index) const { return page_table[s * table_stride + index]; }
+};
+
+hipError_t launch_kv_append(const KvView& kv, const KvStep& st, int64_t seqs, int64_t max_new, const uint16_t* k,
+                            int64_t kt, int64_t kh, const uint16_t* v, int64_t vt, int64_t vh, const float* turns,
+                            int rot, bool interleaved, float magnitude, const uint16_t* q, int64_t qt, int64_t qh,
+                            int q_heads, uint16_t* q_out, hipStream_t s);
+hipError_t launch_kv_read(const KvView& kv, const KvStep& st, int64_t seqs, int64_t max_new, uint16_t* k, uint16_t* v,
+                          hipStream_t s);
+
+size_t attention_workspace_bytes(const KvView& kv, int64_t seqs, int64_t tokens, int64_t max_new, int64_t max_len,
+                                 int64_t q_heads);
+hipError_t launch_attention(const KvView& kv, const KvStep& st, int64_t seqs, int64_t tokens, int64_t max_new,
+                            int64_t max_len, const uint16_t* q, int64_t qt, int64_t qh, int q_heads, float scale,
+                            int64_t window, int64_t sinks, uint16_t* out, float* lse, void* workspace, hipStream_t s);
+
 }  // namespace bl
