@@ -49,7 +49,9 @@ struct Attn {
   int q_heads, group, page_shift;
   int window, sinks;
   float scale;       // of q . k, in base 2
-  int row_tiles;     // 16-row tiles per sequence and head
+  int tile_rows;     // rows of a tile (16 or kPromptRows)
+  int row_tiles;     // tiles per sequence and head
+  int tiles;
   int splits, per;   // workgroups along the keys, steps of each
   uint16_t* out;
   float* lse;
@@ -57,7 +59,18 @@ struct Attn {
   float* part_ml;  // [token][q_head][split][2]
 };
 
-// The rows and steps of one 16-row tile.
+// Wave-uniform values that nothing writes while the kernel runs (page numbers,
+// page scales), through scalar loads: a vector load of one would be waited for
+// together with all key and value loads in flight.
+template <typename T>
+__device__ __forceinline__ T uniform_load(const T* p) {
+  return *reinterpret_cast<const __attribute__((address_space(4))) T*>(reinterpret_cast<uintptr_t>(p));
+}
+__device__ __forceinline__ int64_t page_number(const KvStep& st, int seq, int64_t index) {
+  return uniform_load(st.page_table + seq * st.table_stride + index);
+}
+
+// The rows and steps of one tile.
 struct Tile {
   int seq, head, begin, rows, row0, start;
   int first_pos, last_pos;  // positions of its first and last row
@@ -65,6 +78,21 @@ struct Tile {
   int sink_steps, base, steps;
   __device__ int key0(int step) const { return (step < sink_steps ? step : base + step - sink_steps) * kStep; }
 };
+
+// Workgroups are dealt to the eight XCDs in turn: eight tiles are taken
+// together, split by split, so that all splits of a tile run on one XCD and
+// every XCD gets tiles of all lengths.
+__device__ __forceinline__ bool tile_and_split(const Attn& a, int& index, int& split) {
+  if (a.tiles < 64) {  // too few to spread by eights
+    index = blockIdx.x / a.splits;
+    split = blockIdx.x - index * a.splits;
+    return index < a.tiles;
+  }
+  const int eight = blockIdx.x / (8 * a.splits), rest = blockIdx.x - eight * 8 * a.splits;
+  split = rest >> 3;
+  index = eight * 8 + (rest & 7);
+  return index < a.tiles;
+}
 
 __device__ __forceinline__ bool find_tile(const Attn& a, int index, Tile& t) {
   const int rest = index / a.row_tiles;
@@ -74,11 +102,11 @@ __device__ __forceinline__ bool find_tile(const Attn& a, int index, Tile& t) {
   t.begin = a.st.begin(t.seq);
   const int count = a.st.count(t.seq, t.begin);
   t.rows = count * a.group;
-  t.row0 = rt * 16;
+  t.row0 = rt * a.tile_rows;
   if (t.row0 >= t.rows) return false;
   t.start = a.st.start_of(t.seq);
   t.first_pos = t.start + t.row0 / a.group;
-  t.last_pos = t.start + (min(t.row0 + 16, t.rows) - 1) / a.group;
+  t.last_pos = t.start + (min(t.row0 + a.tile_rows, t.rows) - 1) / a.group;
   const int64_t room = a.st.table_stride << a.page_shift;
   t.keys = (int)min((int64_t)t.last_pos + 1, room);
   const int last = (t.keys + kStep - 1) / kStep;
@@ -98,16 +126,25 @@ __device__ __forceinline__ float groups_sum(float v) {
   return v + __shfl_xor(v, 32, 64);
 }
 
-// A query row of 64 * DC elements (zeros past dim) as high and low bytes; the
-// lane holds elements 64c + 16g .. +15 of row lane % 16.  Returns absmax / 32512.
-template <int DC>
-__device__ __forceinline__ float split_query(const uint16_t* row, bool valid, int dim, int g, v4i (&hi)[DC], v4i (&lo)[DC]) {
-  float x[DC][16], top = 0.0f;
+// the same over lanes l and l ^ 32: v_permlane32_swap of a register with a copy
+// leaves the low half in both halves of one and the high half in the other
+__device__ __forceinline__ float halves_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// A query row (zeros past dim) as high and low bytes, in kChunks chunks of
+// kWidth elements; lane group g of the kWidth / 16 that share a row holds
+// elements kWidth c + 16 g .. +15.  Returns absmax / 32512.
+template <int kWidth, int kChunks>
+__device__ __forceinline__ float split_query(const uint16_t* row, bool valid, int dim, int g, v4i (&hi)[kChunks],
+                                             v4i (&lo)[kChunks]) {
+  float x[kChunks][16], top = 0.0f;
 #pragma unroll
-  for (int c = 0; c < DC; ++c) {
+  for (int c = 0; c < kChunks; ++c) {
     uint4 d[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (valid && 64 * c + 16 * g < dim) {
-      const uint4* p = reinterpret_cast<const uint4*>(row + 64 * c + 16 * g);
+    if (valid && kWidth * c + 16 * g < dim) {
+      const uint4* p = reinterpret_cast<const uint4*>(row + kWidth * c + 16 * g);
       d[0] = p[0];
       d[1] = p[1];
     }
@@ -119,10 +156,11 @@ __device__ __forceinline__ float split_query(const uint16_t* row, bool valid, in
       top = fmaxf(top, fmaxf(fabsf(x[c][2 * i]), fabsf(x[c][2 * i + 1])));
     }
   }
-  top = groups_max(top);
+  if (kWidth == 64) top = fmaxf(top, __shfl_xor(top, 16, 64));
+  top = fmaxf(top, __shfl_xor(top, 32, 64));
   const float s = top > 0x1p-100f ? 32512.0f / top : 0.0f;
 #pragma unroll
-  for (int c = 0; c < DC; ++c) {
+  for (int c = 0; c < kChunks; ++c) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t h = 0, l = 0;
@@ -165,9 +203,10 @@ __global__ __launch_bounds__(kThreads) void k_attn(Attn a) {
   typedef typename VBytes<DC>::type vbytes;
   __shared__ float lds_o[kWaves][16][64 * DC];
   __shared__ float lds_ml[kWaves][16][2];
-  const int split = blockIdx.x % a.splits;
+  int index, split;
+  if (!tile_and_split(a, index, split)) return;
   Tile t;
-  if (!find_tile(a, blockIdx.x / a.splits, t)) return;
+  if (!find_tile(a, index, t)) return;
   const int s0 = split * a.per, s1 = min(t.steps, s0 + a.per);
   if (s0 >= s1) return;
   const bool whole = t.steps <= a.per;
@@ -181,7 +220,7 @@ __global__ __launch_bounds__(kThreads) void k_attn(Attn a) {
   const int pos = t.start + token, low = a.window > 0 ? pos - a.window + 1 : 0;
   v4i qhi[DC], qlo[DC];
   const float row_scale =
-      split_query<DC>(a.q + (int64_t)(t.begin + token) * a.qt + (int64_t)q_head * a.qh, valid, dim, g, qhi, qlo) *
+      split_query<64, DC>(a.q + (int64_t)(t.begin + token) * a.qt + (int64_t)q_head * a.qh, valid, dim, g, qhi, qlo) *
       a.scale * (1.0f / 127.0f);
 
   // byte offsets inside a 16-token tile; elements past dim read element 0
@@ -205,15 +244,15 @@ __global__ __launch_bounds__(kThreads) void k_attn(Attn a) {
     for (int i = 0; i < 4; ++i) {
       const int key = j0 + 16 * i;
       int64_t page = -1;
-      if (key < t.keys) page = a.st.page(t.seq, key >> a.page_shift);
+      if (key < t.keys) page = page_number(a.st, t.seq, key >> a.page_shift);
       dead[i] = page < 0 || page >= a.kv.pages;
       any_dead |= dead[i];
       const int64_t block = dead[i] ? 0 : page * a.kv.heads + t.head;
       const int64_t at = (block * a.kv.page_tokens + (dead[i] ? 0 : key & (a.kv.page_tokens - 1))) * dim;
       kp[i] = a.kv.k + at;
       vp[i] = a.kv.v + at;
-      ka[i] = dead[i] ? 0.0f : a.kv.k_absmax[block];
-      const float top = dead[i] ? 0.0f : a.kv.v_absmax[block];
+      ka[i] = uniform_load(a.kv.k_absmax + block);
+      const float top = dead[i] ? 0.0f : uniform_load(a.kv.v_absmax + block);
       va[i] = top > 0.0f ? top : 1.0f;
     }
     v4i k[4][DC];
@@ -346,13 +385,342 @@ __global__ __launch_bounds__(kThreads) void k_attn(Attn a) {
   if ((tid & 15) == 0) *reinterpret_cast<float2*>(a.part_ml + slot * 2) = make_float2(top, sum);
 }
 
-// Joins the splits of a 16-row tile (tiles of one split are already done).
+// ---- many rows ----
+// One workgroup: 128 query rows (tokens times the heads of a group) of one
+// sequence and cache head, 32 rows per wave, over the steps of one split.  Keys
+// and values of a step (64 tokens) go through LDS, in three buffers: wave w
+// stages tokens 16w .. 16w + 15 while it computes on the step before, K as it
+// is and V already as fp16, so each value is converted once per 128 rows.
+// One team of four waves takes all steps, two workgroups to a CU; or two teams
+// take them in turn, each with its own running state and buffers, one workgroup
+// to a CU, and are joined in LDS at the end (see make_plan for which).
+//   K in LDS: rows of 64 DC bytes, 16-byte chunk c of token m at c ^ key(m), so
+//     that 32 tokens' chunks are read without bank conflicts;
+//   V in LDS: per 16 tokens and MFMA tile t the 64 lanes' operands side by
+//     side; row slot m of tile t is element 2 DC m + t, k-slot 8g + j token
+//     8 (j / 4) + 4g + j % 4, which is how S^T = K Q^T leaves P (g = lane / 32).
+// The running maximum m is raised only when a score passes it by more than
+// kSlack: P is then at most 2^(14 + kSlack) < 65504, and almost every step
+// keeps its O and l as they are.
+typedef int v16i __attribute__((ext_vector_type(16)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+constexpr int kPromptRows = 128;
+constexpr int kRing = 3;
+constexpr float kSlack = 1.5f;
+
+template <int DC>
+__device__ __forceinline__ int k_key(int m) {
+  return DC == 1 ? (m >> 2) & 3 : DC == 2 ? (m >> 1) & 7 : m & 15;
+}
+
+template <int DC>
+struct VPiece;
+template <>
+struct VPiece<1> {
+  typedef uint16_t type;
+  static __device__ uint32_t word(type v, int) { return v; }
+};
+template <>
+struct VPiece<2> {
+  typedef uint32_t type;
+  static __device__ uint32_t word(type v, int) { return v; }
+};
+template <>
+struct VPiece<4> {
+  typedef uint2 type;
+  static __device__ uint32_t word(type v, int c) { return c ? v.y : v.x; }
+};
+
+template <int DC, int kTeams>
+__global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_prompt(Attn a) {
+  typedef typename VPiece<DC>::type vpiece;
+  constexpr int kTiles = 2 * DC;  // 32-element tiles of the head
+  struct Ring {
+    uint4 v[kRing][4 * kTiles * 64];  // [16 tokens][tile][lane]
+    v4i k[kRing][kStep * 4 * DC];     // [token][chunk]
+    float4 scale[kRing][4];           // per 16 tokens: ka, log2 va, 1 / va, there
+  };
+  __shared__ Ring rings[kTeams];
+  int index, split;
+  if (!tile_and_split(a, index, split)) return;
+  Tile t;
+  {  // the longest (last) tiles of all heads first: they end about together
+    const int lists = a.tiles / a.row_tiles, back = index / lists;
+    index = (index - back * lists) * a.row_tiles + (a.row_tiles - 1 - back);
+  }
+  if (!find_tile(a, index, t)) return;
+  const int s0 = split * a.per, s1 = min(t.steps, s0 + a.per);
+  if (s0 >= s1) return;
+  const bool whole = t.steps <= a.per;
+
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5, col = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane((tid >> 6) & 3), team = __builtin_amdgcn_readfirstlane(tid >> 8);
+  const int dim = a.kv.dim, wave_row = t.row0 + 32 * wave, row = wave_row + col;
+  const bool busy = wave_row < t.rows, valid = row < t.rows;
+  const int token = valid ? row / a.group : 0;
+  const int q_head = t.head * a.group + (valid ? row - token * a.group : 0);
+  const int pos = t.start + token, low = a.window > 0 ? pos - a.window + 1 : 0;
+  const int first_pos = t.start + wave_row / a.group, last_pos = t.start + (min(wave_row + 32, t.rows) - 1) / a.group;
+  v4i qhi[kTiles], qlo[kTiles];
+  const float row_scale = split_query<32, kTiles>(a.q + (int64_t)(t.begin + token) * a.qt + (int64_t)q_head * a.qh, valid,
+                                                  dim, g, qhi, qlo) *
+                          a.scale * (1.0f / 127.0f);
+  v16f o[kTiles];
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
+  float m = 0.0f, l = 0.0f;
+  bool started = false;  // m means something: the row has seen a key
+
+  // staging of this wave's 16 tokens of a step
+  Ring& ring = rings[team];
+  v4i k_raw[DC];
+  vpiece v_raw[8];
+  float ka_raw = 0.0f, va_raw = 0.0f;
+  bool there = false;
+  auto page_of = [&](int step) -> int64_t {
+    if (step >= s1) return -1;
+    const int key = t.key0(step) + 16 * wave;
+    return key < t.keys ? page_number(a.st, t.seq, key >> a.page_shift) : -1;
+  };
+  auto load = [&](int step, int64_t page) {
+    const int key = t.key0(step) + 16 * wave;
+    there = page >= 0 && page < a.kv.pages;
+    const int64_t block = there ? page * a.kv.heads + t.head : 0;
+    const int64_t at = (block * a.kv.page_tokens + (there ? key & (a.kv.page_tokens - 1) : 0)) * dim;
+    ka_raw = a.kv.k_absmax[block];
+    va_raw = a.kv.v_absmax[block];
+    const int8_t* kp = a.kv.k + at;
+    const int8_t* vp = a.kv.v + at + (4 * g) * dim + (2 * DC * col < dim ? 2 * DC * col : 0);
+#pragma unroll
+    for (int i = 0; i < DC; ++i) {
+      const int unit = lane + 64 * i, tok = unit / (4 * DC), c = unit % (4 * DC);
+      k_raw[i] = *reinterpret_cast<const v4i*>(kp + tok * dim + (16 * c < dim ? 16 * c : 0));
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v_raw[j] = *reinterpret_cast<const vpiece*>(vp + (8 * (j >> 2) + (j & 3)) * dim);
+  };
+  auto store = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < DC; ++i) {
+      const int unit = lane + 64 * i, tok = 16 * wave + unit / (4 * DC), c = unit % (4 * DC);
+      ring.k[buf][tok * 4 * DC + (c ^ k_key<DC>(tok))] = k_raw[i];
+    }
+    uint32_t w[8][(DC + 1) / 2];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int c = 0; c < (DC + 1) / 2; ++c) w[j][c] = VPiece<DC>::word(v_raw[j], c) ^ 0x80808080u;
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      ring.v[buf][(wave * kTiles + i) * 64 + lane] =
+          make_uint4(halves_of(w[0][i >> 2], w[1][i >> 2], i & 3), halves_of(w[2][i >> 2], w[3][i >> 2], i & 3),
+                     halves_of(w[4][i >> 2], w[5][i >> 2], i & 3), halves_of(w[6][i >> 2], w[7][i >> 2], i & 3));
+    }
+    if (lane == 0) {
+      const float va = there && va_raw > 0.0f ? va_raw : 1.0f;
+      ring.scale[buf][wave] = make_float4(ka_raw, __builtin_amdgcn_logf(va), __builtin_amdgcn_rcpf(va), there ? 1.0f : 0.0f);
+    }
+  };
+
+  // products of the two 32-key halves of a step; heads past 128 elements have
+  // no registers left to hold one half's while the other's are made
+  constexpr bool kAhead = DC <= 2;
+  v16i high[2], lo[2];
+  auto product = [&](int buf, int h) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) high[h][j] = 0, lo[h][j] = 0;
+    const int tok = 32 * h + col;
+#pragma unroll
+    for (int c = 0; c < kTiles; ++c) {
+      const v4i kf = ring.k[buf][tok * 4 * DC + ((2 * c + g) ^ k_key<DC>(tok))];
+      high[h] = __builtin_amdgcn_mfma_i32_32x32x32_i8(kf, qhi[c], high[h], 0, 0, 0);
+      lo[h] = __builtin_amdgcn_mfma_i32_32x32x32_i8(kf, qlo[c], lo[h], 0, 0, 0);
+    }
+  };
+  // half h of the step in buffer buf; the products of the following half (of
+  // buffer next) are issued among its vector instructions
+  auto half = [&](int step, int buf, auto which, int next) {
+    constexpr int h = decltype(which)::value;
+    const int j0 = t.key0(step);
+    const float4 sc[2] = {ring.scale[buf][2 * h], ring.scale[buf][2 * h + 1]};
+    // wave-uniform: whether all of its rows see all of the half
+    const bool all = j0 + 32 * h + 32 <= min(first_pos + 1, t.keys) &&
+                     (a.window == 0 || j0 + 32 * h > last_pos - a.window || j0 + 32 * h + 32 <= a.sinks) &&
+                     __builtin_amdgcn_readfirstlane(sc[0].w * sc[1].w != 0.0f);
+    float x[16], top;
+    product(kAhead ? next : buf, kAhead ? h ^ 1 : h);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const float mul = row_scale * sc[b].x, add = sc[b].y + (14.0f - m);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        x[8 * b + j] = __builtin_fmaf((float)(high[h][8 * b + j] * 256 + lo[h][8 * b + j]), mul, add);
+    }
+    if (!all) {
+      asm volatile("; masked keys");  // stays a branch: most steps need none of this
+      const int at = j0 + 32 * h + 4 * g, past = min(pos, t.keys - 1) - at, before = low - at, first = a.sinks - at;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int key = 8 * (j >> 2) + (j & 3);
+        const bool seen = key <= past && (key >= before || key < first) && sc[j >> 3].w != 0.0f;
+        x[j] = seen ? x[j] : -INFINITY;
+      }
+    }
+    top = kNone;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) top = fmaxf(top, x[j]);
+    top = halves_max(top);
+    if (__any(top > 14.0f + kSlack || (!started && top > kNone))) {
+      // lanes whose maximum grew (or that see their first key) take it
+      asm volatile("; raised maximum");
+      const bool grows = started ? top > 14.0f : top > kNone;
+      const float delta = grows ? top - 14.0f : 0.0f;
+      const float shrink = started ? __builtin_amdgcn_exp2f(-delta) : 0.0f;
+      m += delta;
+      started |= grows;
+      l *= shrink;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[j] -= delta;
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] *= shrink;
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      v8h pf;
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float p = __builtin_amdgcn_exp2f(x[8 * b + j]);
+        sum += p;
+        pf[j] = (_Float16)p;
+      }
+      l = __builtin_fmaf(sum, sc[b].z, l);
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) {
+        const uint4 raw = ring.v[buf][((2 * h + b) * kTiles + i) * 64 + lane];
+        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, raw), pf, o[i], 0, 0, 0);
+      }
+    }
+  };
+
+  // A team's step is staged while the first half of the one before is worked
+  // on, behind one barrier per step: a wave that stores the n-th has passed the
+  // barrier in the (n - 2)-th, so every wave is done with the (n - 3)-th, whose
+  // buffer (of three) it takes.
+  constexpr int kStride = kTeams;
+  const int rounds = (s1 - s0 + kStride - 1) / kStride;
+  int step = s0 + team, buf = 0;
+  int64_t next_page = page_of(step);
+  if (step < s1) {
+    load(step, next_page);
+    next_page = page_of(step + kStride);
+    store(0);
+  }
+  if (step + kStride < s1) {
+    load(step + kStride, next_page);
+    next_page = page_of(step + 2 * kStride);
+  }
+  __syncthreads();
+  if (kAhead && busy && step < s1) product(0, 0);
+  for (int round = 0; round < rounds; ++round, step += kStride) {
+    const int next = buf == kRing - 1 ? 0 : buf + 1;
+    const bool mine = busy && step < s1;
+    if (mine) half(step, buf, std::integral_constant<int, 0>{}, buf);
+    if (step + kStride < s1) store(next);
+    __syncthreads();
+    if (step + 2 * kStride < s1) {
+      load(step + 2 * kStride, next_page);
+      next_page = page_of(step + 3 * kStride);
+    }
+    // (after the last step the products of a stale buffer are not used)
+    if (mine) half(step, buf, std::integral_constant<int, 1>{}, next);
+    buf = next;
+  }
+
+  l += __shfl_xor(l, 32, 64);
+  if (kTeams == 2) {
+    // the second team's rows meet the first's, lane by lane
+    float4* out = reinterpret_cast<float4*>(&rings[1].v[0][0]) + wave * 4 * kTiles * 64 + lane;
+    float2* out_ml = reinterpret_cast<float2*>(&rings[0].v[0][0]) + wave * 64 + lane;
+    __syncthreads();
+    if (team == 1) {
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          out[(4 * i + b) * 64] = make_float4(o[i][4 * b], o[i][4 * b + 1], o[i][4 * b + 2], o[i][4 * b + 3]);
+      *out_ml = make_float2(started ? m : kNone, l);
+    }
+    __syncthreads();
+    if (team == 1) return;
+    const float2 ml = *out_ml;
+    const float mine = started ? m : kNone, top = fmaxf(mine, ml.x);
+    const float w0 = __builtin_amdgcn_exp2f(mine - top), w1 = __builtin_amdgcn_exp2f(ml.x - top);
+    l = l * w0 + ml.y * w1;
+    m = top;
+    started = top > kNone;
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float4 f = out[(4 * i + b) * 64];
+        o[i][4 * b] = o[i][4 * b] * w0 + f.x * w1;
+        o[i][4 * b + 1] = o[i][4 * b + 1] * w0 + f.y * w1;
+        o[i][4 * b + 2] = o[i][4 * b + 2] * w0 + f.z * w1;
+        o[i][4 * b + 3] = o[i][4 * b + 3] * w0 + f.w * w1;
+      }
+  }
+  if (!valid) return;
+  const int64_t out_row = (int64_t)(t.begin + token) * a.q_heads + q_head;
+  const float mul = l > 0.0f ? (512.0f / 127.0f) / l : 0.0f;
+  const int64_t slot = out_row * a.splits + split;
+  // o[i][4b + j] is element 2 DC (8b + 4g + j) + i: 8 DC adjacent ones per b
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const int at = 2 * DC * (8 * b + 4 * g);
+    if (at >= dim) break;
+    float y[8 * DC];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) y[kTiles * j + i] = o[i][4 * b + j];
+    if (whole) {
+      uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * dim + at);
+#pragma unroll
+      for (int i = 0; i < DC && at + 8 * i < dim; ++i)  // dim is a multiple of 16
+        dst[i] = make_uint4(f32x2_to_bf16x2(y[8 * i] * mul, y[8 * i + 1] * mul),
+                            f32x2_to_bf16x2(y[8 * i + 2] * mul, y[8 * i + 3] * mul),
+                            f32x2_to_bf16x2(y[8 * i + 4] * mul, y[8 * i + 5] * mul),
+                            f32x2_to_bf16x2(y[8 * i + 6] * mul, y[8 * i + 7] * mul));
+    } else {
+      float4* dst = reinterpret_cast<float4*>(a.part_o + slot * dim + at);
+#pragma unroll
+      for (int i = 0; i < 2 * DC && at + 4 * i < dim; ++i)
+        dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+    }
+  }
+  if (g == 0) {
+    if (!whole)
+      *reinterpret_cast<float2*>(a.part_ml + slot * 2) = make_float2(started ? m : kNone, l);
+    else if (a.lse)
+      a.lse[out_row] = l > 0.0f ? (__log2f(l) + m - 14.0f) * kLn2 : -INFINITY;
+  }
+}
+
+// Joins the splits of 16 rows of a tile (tiles of one split are already done).
 template <int DC>
 __global__ __launch_bounds__(kThreads) void k_attn_join(Attn a) {
   Tile t;
-  if (!find_tile(a, blockIdx.x, t) || t.steps <= a.per) return;
+  const int pieces = a.tile_rows / 16, tile = blockIdx.x / pieces;
+  if (!find_tile(a, tile, t) || t.steps <= a.per) return;
   const int splits = (t.steps + a.per - 1) / a.per;
-  const int tid = threadIdx.x, r = tid >> 4, seg = (tid & 15) * 4 * DC, dim = a.kv.dim;
+  const int tid = threadIdx.x, r = (blockIdx.x - tile * pieces) * 16 + (tid >> 4), seg = (tid & 15) * 4 * DC;
+  const int dim = a.kv.dim;
   if (t.row0 + r >= t.rows) return;
   const int tok = (t.row0 + r) / a.group;
   const int64_t out_row = (int64_t)(t.begin + tok) * a.q_heads + t.head * a.group + (t.row0 + r - tok * a.group);
@@ -386,32 +754,52 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(Attn a) {
   if (a.lse && (tid & 15) == 0) a.lse[out_row] = sum > 0.0f ? (__log2f(sum) + top - 14.0f) * kLn2 : -INFINITY;
 }
 
+// Rows from which the workgroups of 128 rows take over from those of 16.
+constexpr int64_t kPromptFrom = 64;
+
 // Workgroups along the keys: enough to fill the chip, none with less than a
 // step per wave.  The split is a number of steps, the same for every sequence
 // of the batch, so a short sequence takes fewer workgroups and not shorter ones.
-constexpr int64_t kTargetBlocks = 2048;
+constexpr int64_t kTargetBlocks = 2048, kTargetPromptBlocks = 512;
 
 struct Plan {
+  int tile_rows;
   int64_t row_tiles, tiles;
+  int64_t most_splits;  // of any window
   int splits, per;
+  int teams;  // of a workgroup of 128 rows
 };
+
+// Two teams (one workgroup of eight waves to a CU) while the tiles fill the
+// 256 CUs less than twice and each has many steps: a tile then takes half the
+// time (376 tiles of up to 94 steps: 133 us against 185 with one team, 256 of 47:
+// 68 against 79, 480 of 103: 182 against 207).  One team (two independent
+// workgroups to a CU) where there are tiles enough (940 of up to 94: 290 us
+// against 302) or few steps (480 of 20: 65 against 73, 96 of 7: 21 against 26).
+bool two_teams(int dim, int64_t tiles, int64_t steps) { return dim <= 128 && tiles < 512 && steps > 24; }
 
 Plan make_plan(const KvView& kv, int64_t seqs, int64_t max_new, int64_t max_len, int64_t q_heads, int64_t window,
                int64_t sinks) {
   Plan p;
-  p.row_tiles = (max_new * (q_heads / kv.heads) + 15) / 16;
+  const int64_t rows = max_new * (q_heads / kv.heads);
+  p.tile_rows = rows >= kPromptFrom ? kPromptRows : 16;
+  p.row_tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   p.tiles = seqs * kv.heads * p.row_tiles;
+  auto splits_of = [&](int64_t steps, int64_t target) {
+    const int64_t wanted = p.tiles < target ? target / p.tiles : 1, most = (steps + kWaves - 1) / kWaves;
+    return wanted < most ? wanted : most;
+  };
   int64_t steps = (max_len + kStep - 1) / kStep;
+  const int64_t target = p.tile_rows == 16 ? kTargetBlocks : kTargetPromptBlocks;
+  p.most_splits = splits_of(steps, target);
   if (window > 0) {
-    const int64_t most = (window + 16 + kStep) / kStep + 1 + (sinks + kStep - 1) / kStep;
+    const int64_t most = (window + p.tile_rows + kStep) / kStep + 1 + (sinks + kStep - 1) / kStep;
     if (most < steps) steps = most;
   }
-  int64_t splits = (kTargetBlocks + p.tiles - 1) / p.tiles;
-  const int64_t most = (steps + kWaves - 1) / kWaves;
-  if (splits > most) splits = most;
-  if (splits < 1) splits = 1;
+  p.teams = p.tile_rows != 16 && two_teams(kv.dim, p.tiles, steps) ? 2 : 1;
+  const int64_t splits = splits_of(steps, target / p.teams);
   p.per = (int)((steps + splits - 1) / splits);
-  p.splits = (int)((steps + p.per - 1) / p.per);
+  p.splits = (int)((steps + p.per - 1) / p.per);  // at most splits, so at most most_splits
   return p;
 }
 
@@ -419,16 +807,16 @@ Plan make_plan(const KvView& kv, int64_t seqs, int64_t max_new, int64_t max_len,
 
 size_t attention_workspace_bytes(const KvView& kv, int64_t seqs, int64_t tokens, int64_t max_new, int64_t max_len,
                                  int64_t q_heads) {
-  // without a window there are the most splits
   const Plan p = make_plan(kv, seqs, max_new, max_len, q_heads, 0, 0);
-  return p.splits <= 1 ? 0 : (size_t)tokens * (size_t)q_heads * (size_t)p.splits * (size_t)(kv.dim + 2) * 4;
+  return p.most_splits <= 1 ? 0 : (size_t)tokens * (size_t)q_heads * (size_t)p.most_splits * (size_t)(kv.dim + 2) * 4;
 }
 
 hipError_t launch_attention(const KvView& kv, const KvStep& st, int64_t seqs, int64_t tokens, int64_t max_new,
                             int64_t max_len, const uint16_t* q, int64_t qt, int64_t qh, int q_heads, float scale,
                             int64_t window, int64_t sinks, uint16_t* out, float* lse, void* workspace, hipStream_t s) {
   const Plan p = make_plan(kv, seqs, max_new, max_len, q_heads, window, sinks);
-  if (!grid_fits(p.tiles * p.splits, kThreads)) return kErrGridTooLarge;
+  const int64_t blocks = (p.tiles + 7) / 8 * 8 * p.splits;
+  if (!grid_fits(blocks, 2 * kThreads) || !grid_fits(p.tiles * (p.tile_rows / 16), kThreads)) return kErrGridTooLarge;
   Attn a;
   a.kv = kv;
   a.st = st;
@@ -441,7 +829,9 @@ hipError_t launch_attention(const KvView& kv, const KvStep& st, int64_t seqs, in
   a.window = (int)window;
   a.sinks = (int)sinks;
   a.scale = scale * kLog2e;
+  a.tile_rows = p.tile_rows;
   a.row_tiles = (int)p.row_tiles;
+  a.tiles = (int)p.tiles;
   a.splits = p.splits;
   a.per = p.per;
   a.out = out;
@@ -450,10 +840,23 @@ hipError_t launch_attention(const KvView& kv, const KvStep& st, int64_t seqs, in
   a.part_ml = a.part_o + tokens * q_heads * p.splits * kv.dim;
   auto go = [&](auto dc) {
     constexpr int DC = decltype(dc)::value;
-    hipLaunchKernelGGL(k_attn<DC>, dim3((unsigned)(p.tiles * p.splits)), dim3(kThreads), 0, s, a);
+    auto prompt = [&](int teams) {
+      if constexpr (DC <= 2) {
+        if (teams == 2) {
+          hipLaunchKernelGGL((k_attn_prompt<DC, 2>), dim3((unsigned)blocks), dim3(2 * kThreads), 0, s, a);
+          return;
+        }
+      }
+      hipLaunchKernelGGL((k_attn_prompt<DC, 1>), dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
+    };
+    const dim3 grid((unsigned)blocks), pieces((unsigned)(p.tiles * (p.tile_rows / 16)));
+    if (p.tile_rows == 16)
+      hipLaunchKernelGGL(k_attn<DC>, grid, dim3(kThreads), 0, s, a);
+    else
+      prompt(p.teams);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits <= 1) return e;
-    hipLaunchKernelGGL(k_attn_join<DC>, dim3((unsigned)p.tiles), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL(k_attn_join<DC>, pieces, dim3(kThreads), 0, s, a);
     return hipGetLastError();
   };
   if (kv.dim <= 64) return go(std::integral_constant<int, 1>{});
