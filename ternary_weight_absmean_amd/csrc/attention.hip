@@ -116,21 +116,18 @@ __device__ __forceinline__ bool find_tile(const Attn& a, int index, Tile& t) {
   return true;
 }
 
-// reductions over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48)
-__device__ __forceinline__ float groups_max(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16, 64));
-  return fmaxf(v, __shfl_xor(v, 32, 64));
-}
-__device__ __forceinline__ float groups_sum(float v) {
-  v += __shfl_xor(v, 16, 64);
-  return v + __shfl_xor(v, 32, 64);
-}
-
-// the same over lanes l and l ^ 32: v_permlane32_swap of a register with a copy
-// leaves the low half in both halves of one and the high half in the other
+// Largest value over lanes l and l ^ 32: v_permlane32_swap of a register with
+// a copy leaves the low half in both halves of one and the high half in both of
+// the other.
 __device__ __forceinline__ float halves_max(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// The same over the four rows of 16 lanes (l, l ^ 16, l ^ 32, l ^ 48).
+__device__ __forceinline__ float rows_max(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return halves_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
 }
 
 // A query row (zeros past dim) as high and low bytes, in kChunks chunks of
@@ -186,20 +183,40 @@ __device__ __forceinline__ uint32_t halves_of(uint32_t w0, uint32_t w1, int b) {
   return __builtin_bit_cast(uint32_t, scaled);
 }
 
+// The 4 DC adjacent bytes of a token that a lane of k_attn reads, by words.
 template <int DC>
 struct VBytes;
 template <>
-struct VBytes<1> { typedef uint32_t type; };
+struct VBytes<1> {
+  typedef uint32_t type;
+  static __device__ uint32_t word(type v, int) { return v; }
+};
 template <>
-struct VBytes<2> { typedef uint2 type; };
+struct VBytes<2> {
+  typedef uint32_t type __attribute__((ext_vector_type(2)));
+  static __device__ uint32_t word(type v, int c) { return v[c]; }
+};
 template <>
-struct VBytes<4> { typedef uint4 type; };
+struct VBytes<4> {
+  typedef uint32_t type __attribute__((ext_vector_type(4)));
+  static __device__ uint32_t word(type v, int c) { return v[c]; }
+};
+
+// The running maximum m is raised only when a score passes it by more than
+// this: P is then at most 2^(14 + kSlack) < 65504, and almost every step keeps
+// its O and l as they are.
+constexpr float kSlack = 1.5f;
 
 // One workgroup: 16 query rows of one sequence and cache head, the steps of
 // one split; wave w takes steps w, w + 4, ... with its own running state, and
-// the waves' states are joined in LDS at the end.
-template <int DC>
-__global__ __launch_bounds__(kThreads) void k_attn(Attn a) {
+// the waves' states are joined in LDS at the end.  A step's keys and values go
+// straight into registers; the next step's keys are asked for as soon as the
+// products have read this step's, its values as soon as those are converted, so
+// that loads are in flight nearly all the time without a second set of
+// registers.  kPages: pages that 64 tokens lie in (1, or 4 for pages of 16 and
+// 32 tokens, looked up for each 16 tokens).
+template <int DC, int kPages>
+__global__ __launch_bounds__(kThreads, DC == 1 ? 4 : DC == 2 ? (kPages == 1 ? 3 : 2) : 1) void k_attn(Attn a) {
   typedef typename VBytes<DC>::type vbytes;
   __shared__ float lds_o[kWaves][16][64 * DC];
   __shared__ float lds_ml[kWaves][16][2];
@@ -218,10 +235,6 @@ __global__ __launch_bounds__(kThreads) void k_attn(Attn a) {
   const int token = valid ? row / a.group : 0;
   const int q_head = t.head * a.group + (valid ? row - token * a.group : 0);
   const int pos = t.start + token, low = a.window > 0 ? pos - a.window + 1 : 0;
-  v4i qhi[DC], qlo[DC];
-  const float row_scale =
-      split_query<64, DC>(a.q + (int64_t)(t.begin + token) * a.qt + (int64_t)q_head * a.qh, valid, dim, g, qhi, qlo) *
-      a.scale * (1.0f / 127.0f);
 
   // byte offsets inside a 16-token tile; elements past dim read element 0
   // instead (their query bytes are zero, their outputs are not stored)
@@ -230,115 +243,180 @@ __global__ __launch_bounds__(kThreads) void k_attn(Attn a) {
   for (int c = 0; c < DC; ++c) koff[c] = (uint32_t)(col * dim + (64 * c + 16 * g < dim ? 64 * c + 16 * g : 0));
   voff = (uint32_t)(4 * g * dim + (4 * DC * col < dim ? 4 * DC * col : 0));
 
+  struct Place {  // of a step's keys and values
+    int64_t at[kPages];
+    float ka[kPages], va[kPages];
+    bool there[kPages];
+  };
+  auto look_up = [&](int step, int64_t(&page)[kPages]) {
+#pragma unroll
+    for (int i = 0; i < kPages; ++i) {
+      const int key = step < s1 ? t.key0(step) + kStep / kPages * i : t.keys;
+      page[i] = key < t.keys ? page_number(a.st, t.seq, key >> a.page_shift) : -1;
+    }
+  };
+  auto place = [&](int step, const int64_t(&page)[kPages], Place& p) {
+#pragma unroll
+    for (int i = 0; i < kPages; ++i) {
+      const int key = t.key0(step) + kStep / kPages * i;
+      p.there[i] = page[i] >= 0 && page[i] < a.kv.pages;
+      const int64_t block = p.there[i] ? page[i] * a.kv.heads + t.head : 0;
+      p.at[i] = (block * a.kv.page_tokens + (p.there[i] ? key & (a.kv.page_tokens - 1) : 0)) * dim;
+      p.ka[i] = uniform_load(a.kv.k_absmax + block);
+      p.va[i] = uniform_load(a.kv.v_absmax + block);
+    }
+  };
+  v4i k[4][DC];
+  vbytes v[4][4];
+  // a page of 16 or 32 tokens that is not there is read from the first page's
+  // start; with one page per step its 64 tokens are there too
+  auto load_k = [&](const Place& p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int8_t* from = a.kv.k + p.at[i * kPages / 4] + (kPages == 1 ? i * 16 * dim : 0);
+#pragma unroll
+      for (int c = 0; c < DC; ++c) k[i][c] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(from + koff[c]));
+    }
+  };
+  auto load_v = [&](const Place& p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int8_t* from = a.kv.v + p.at[i * kPages / 4] + (kPages == 1 ? i * 16 * dim : 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i][j] = __builtin_nontemporal_load(reinterpret_cast<const vbytes*>(from + voff + j * dim));
+    }
+  };
+
+  int step = s0 + wave;
+  int64_t page[kPages];
+  Place now, then;
+  look_up(step, page);
+  if (step < s1) {
+    place(step, page, now);
+    load_k(now);
+    load_v(now);
+  }
+  look_up(step + kWaves, page);
+  v4i qhi[DC], qlo[DC];
+  const float row_scale =
+      split_query<64, DC>(a.q + (int64_t)(t.begin + token) * a.qt + (int64_t)q_head * a.qh, valid, dim, g, qhi, qlo) *
+      a.scale * (1.0f / 127.0f);
+
   v4f o[4 * DC];
 #pragma unroll
   for (int i = 0; i < 4 * DC; ++i) o[i] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-  float m = kNone, l = 0.0f;
+  float m = 0.0f, l = 0.0f;
+  bool started = false;  // m means something: the row has seen a key
 
-  for (int step = s0 + wave; step < s1; step += kWaves) {
+  for (; step < s1; step += kWaves) {
     const int j0 = t.key0(step);
-    const int8_t *kp[4], *vp[4];
-    float ka[4], va[4];
-    bool dead[4], any_dead = false;
+    const bool more = step + kWaves < s1;
+    float x[4][4], va[kPages];
+    bool all = j0 + kStep <= min(t.first_pos + 1, t.keys) &&
+               (a.window == 0 || j0 > t.last_pos - a.window || j0 + kStep <= a.sinks);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int key = j0 + 16 * i;
-      int64_t page = -1;
-      if (key < t.keys) page = page_number(a.st, t.seq, key >> a.page_shift);
-      dead[i] = page < 0 || page >= a.kv.pages;
-      any_dead |= dead[i];
-      const int64_t block = dead[i] ? 0 : page * a.kv.heads + t.head;
-      const int64_t at = (block * a.kv.page_tokens + (dead[i] ? 0 : key & (a.kv.page_tokens - 1))) * dim;
-      kp[i] = a.kv.k + at;
-      vp[i] = a.kv.v + at;
-      ka[i] = uniform_load(a.kv.k_absmax + block);
-      const float top = dead[i] ? 0.0f : uniform_load(a.kv.v_absmax + block);
-      va[i] = top > 0.0f ? top : 1.0f;
+    for (int i = 0; i < kPages; ++i) {
+      all = all && now.there[i];
+      va[i] = now.there[i] && now.va[i] > 0.0f ? now.va[i] : 1.0f;
     }
-    v4i k[4][DC];
-    vbytes v[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int c = 0; c < DC; ++c) k[i][c] = *reinterpret_cast<const v4i*>(kp[i] + koff[c]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[i][j] = *reinterpret_cast<const vbytes*>(vp[i] + voff + j * dim);
-
-    float p[4][4], top = kNone;
-    const bool all = !any_dead && j0 + kStep <= t.first_pos + 1 && j0 + kStep <= t.keys &&
-                     (a.window == 0 || j0 > t.last_pos - a.window || j0 + kStep <= a.sinks);
+    v4i high[4], lo[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v4i high = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
+      high[i] = lo[i] = (v4i){0, 0, 0, 0};
 #pragma unroll
       for (int c = 0; c < DC; ++c) {
-        high = mfma_16x16x64(k[i][c], qhi[c], high);
-        lo = mfma_16x16x64(k[i][c], qlo[c], lo);
+        high[i] = mfma_16x16x64(k[i][c], qhi[c], high[i]);
+        lo[i] = mfma_16x16x64(k[i][c], qlo[c], lo[i]);
       }
-      const float mul = row_scale * ka[i], add = __builtin_amdgcn_logf(va[i]);
+    }
+    if (more) {
+      place(step + kWaves, page, then);
+      load_k(then);
+    }
+    float top = kNone;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[i][j] = __builtin_fmaf((float)(high[j] * 256 + lo[j]), mul, add);
-      if (!all) {
+    for (int i = 0; i < 4; ++i) {
+      const float mul = row_scale * now.ka[i * kPages / 4], add = __builtin_amdgcn_logf(va[i * kPages / 4]) + (14.0f - m);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[i][j] = __builtin_fmaf((float)(high[i][j] * 256 + lo[i][j]), mul, add);
+    }
+    if (!all) {
+      asm volatile("; masked keys");  // stays a branch: most steps need none of this
+      const int at = j0 + 4 * g, past = min(pos, t.keys - 1) - at, before = low - at, first = a.sinks - at;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int key = j0 + 16 * i + 4 * g + j;
-          const bool seen = !dead[i] && key <= pos && key < t.keys && (key >= low || key < a.sinks);
-          p[i][j] = seen ? p[i][j] : -INFINITY;
+          const int key = 16 * i + j;
+          const bool seen = key <= past && (key >= before || key < first) && now.there[i * kPages / 4];
+          x[i][j] = seen ? x[i][j] : -INFINITY;
         }
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) top = fmaxf(top, p[i][j]);
     }
-    const float m_new = fmaxf(m, groups_max(top));
-    const float shrink = __builtin_amdgcn_exp2f(m - m_new);
-    m = m_new;
-    l *= shrink;
 #pragma unroll
-    for (int i = 0; i < 4 * DC; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[i][j] *= shrink;
+      for (int j = 0; j < 4; ++j) top = fmaxf(top, x[i][j]);
+    top = rows_max(top);
+    if (__any(top > 14.0f + kSlack || (!started && top > kNone))) {
+      // lanes whose maximum grew (or that see their first key) take it
+      asm volatile("; raised maximum");
+      const bool grows = started ? top > 14.0f : top > kNone;
+      const float delta = grows ? top - 14.0f : 0.0f;
+      const float shrink = started ? __builtin_amdgcn_exp2f(-delta) : 0.0f;
+      m += delta;
+      started |= grows;
+      l *= shrink;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[i][j] -= delta;
+#pragma unroll
+      for (int i = 0; i < 4 * DC; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][j] *= shrink;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        p[i][j] = __builtin_amdgcn_exp2f(p[i][j] - m + 14.0f);
-        sum += p[i][j];
+        x[i][j] = __builtin_amdgcn_exp2f(x[i][j]);
+        sum += x[i][j];
       }
-      l = __builtin_fmaf(sum, __builtin_amdgcn_rcpf(va[i]), l);
+      l = __builtin_fmaf(sum, __builtin_amdgcn_rcpf(va[i * kPages / 4]), l);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       v8h pf;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        pf[j] = (_Float16)p[2 * h][j];
-        pf[4 + j] = (_Float16)p[2 * h + 1][j];
-      }
-      uint32_t w[8][DC];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const vbytes raw = v[2 * h + (j >> 2)][j & 3];
-        __builtin_memcpy(w[j], &raw, sizeof(raw));
-#pragma unroll
-        for (int c = 0; c < DC; ++c) w[j][c] ^= 0x80808080u;
+        pf[j] = (_Float16)x[2 * h][j];
+        pf[4 + j] = (_Float16)x[2 * h + 1][j];
       }
 #pragma unroll
-      for (int i = 0; i < 4 * DC; ++i) {
-        uint32_t f[4];
+      for (int c = 0; c < DC; ++c) {
+        uint32_t w[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = halves_of(w[2 * j][i >> 2], w[2 * j + 1][i >> 2], i & 3);
-        v8h vf;
-        __builtin_memcpy(&vf, f, 16);
-        o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf, o[i], 0, 0, 0);
+        for (int j = 0; j < 8; ++j) w[j] = VBytes<DC>::word(v[2 * h + (j >> 2)][j & 3], c) ^ 0x80808080u;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint4 f = make_uint4(halves_of(w[0], w[1], b), halves_of(w[2], w[3], b), halves_of(w[4], w[5], b),
+                                     halves_of(w[6], w[7], b));
+          o[4 * c + b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, f), pf, o[4 * c + b], 0, 0, 0);
+        }
       }
+    }
+    if (more) {
+      load_v(then);
+      now = then;
+      look_up(step + 2 * kWaves, page);
     }
   }
 
   // join the waves: o[i][j] of the lane is element 16 DC g + 4 DC j + i of its row
-  l = groups_sum(l);
+  l += __shfl_xor(l, 16, 64);
+  l += __shfl_xor(l, 32, 64);
+  m = started ? m : kNone;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -399,15 +477,11 @@ __global__ __launch_bounds__(kThreads) void k_attn(Attn a) {
 //   V in LDS: per 16 tokens and MFMA tile t the 64 lanes' operands side by
 //     side; row slot m of tile t is element 2 DC m + t, k-slot 8g + j token
 //     8 (j / 4) + 4g + j % 4, which is how S^T = K Q^T leaves P (g = lane / 32).
-// The running maximum m is raised only when a score passes it by more than
-// kSlack: P is then at most 2^(14 + kSlack) < 65504, and almost every step
-// keeps its O and l as they are.
 typedef int v16i __attribute__((ext_vector_type(16)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr int kPromptRows = 128;
 constexpr int kRing = 3;
-constexpr float kSlack = 1.5f;
 
 template <int DC>
 __device__ __forceinline__ int k_key(int m) {
@@ -712,46 +786,64 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
   }
 }
 
-// Joins the splits of 16 rows of a tile (tiles of one split are already done).
-template <int DC>
+// Joins the splits of a row (rows of one split are already done): kRowWaves
+// waves per row, whose lanes take four elements each and, 16 DC lanes apart,
+// different splits.  One wave per row for up to eight splits; four for more,
+// where a row's partial sums are a serial chain of loads otherwise.
+template <int DC, int kRowWaves>
 __global__ __launch_bounds__(kThreads) void k_attn_join(Attn a) {
+  constexpr int kRows = kWaves / kRowWaves, kLanes = 16 * DC, kGroups = 64 / kLanes;
+  __shared__ v4f lds_x[kWaves][kLanes];
+  __shared__ float lds_sum[kWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, dim = a.kv.dim;
+  const int pieces = a.tile_rows / kRows, tile = blockIdx.x / pieces;
+  const int r = (blockIdx.x - tile * pieces) * kRows + wave / kRowWaves;
   Tile t;
-  const int pieces = a.tile_rows / 16, tile = blockIdx.x / pieces;
   if (!find_tile(a, tile, t) || t.steps <= a.per) return;
-  const int splits = (t.steps + a.per - 1) / a.per;
-  const int tid = threadIdx.x, r = (blockIdx.x - tile * pieces) * 16 + (tid >> 4), seg = (tid & 15) * 4 * DC;
-  const int dim = a.kv.dim;
-  if (t.row0 + r >= t.rows) return;
-  const int tok = (t.row0 + r) / a.group;
-  const int64_t out_row = (int64_t)(t.begin + tok) * a.q_heads + t.head * a.group + (t.row0 + r - tok * a.group);
+  const int splits = (t.steps + a.per - 1) / a.per, row = t.row0 + r;
+  const bool valid = row < t.rows;
+  const int tok = valid ? row / a.group : 0;
+  const int64_t out_row = (int64_t)(t.begin + tok) * a.q_heads + t.head * a.group + (valid ? row - tok * a.group : 0);
   const float* ml = a.part_ml + out_row * a.splits * 2;
   float top = kNone;
-  for (int i = 0; i < splits; ++i) top = fmaxf(top, ml[2 * i]);
-  float sum = 0.0f, x[4 * DC];
-#pragma unroll
-  for (int i = 0; i < 4 * DC; ++i) x[i] = 0.0f;
-  for (int i = 0; i < splits; ++i) {
+  for (int i = lane; valid && i < splits; i += 64) top = fmaxf(top, ml[2 * i]);
+  top = rows_max(top);
+  for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+  const int at = (lane & (kLanes - 1)) * 4;
+  float sum = 0.0f;
+  v4f x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int i = (wave % kRowWaves) * kGroups + lane / kLanes; i < splits; i += kRowWaves * kGroups) {
+    if (!valid) break;
     const float weight = __builtin_amdgcn_exp2f(ml[2 * i] - top);
+    const v4f f = *reinterpret_cast<const v4f*>(a.part_o + (out_row * a.splits + i) * dim + (at < dim ? at : 0));
     sum = __builtin_fmaf(weight, ml[2 * i + 1], sum);
-    if (seg < dim) {
-      const float4* src = reinterpret_cast<const float4*>(a.part_o + (out_row * a.splits + i) * dim + seg);
 #pragma unroll
-      for (int j = 0; j < DC; ++j) {
-        const float4 f = src[j];
-        x[4 * j] = __builtin_fmaf(weight, f.x, x[4 * j]);
-        x[4 * j + 1] = __builtin_fmaf(weight, f.y, x[4 * j + 1]);
-        x[4 * j + 2] = __builtin_fmaf(weight, f.z, x[4 * j + 2]);
-        x[4 * j + 3] = __builtin_fmaf(weight, f.w, x[4 * j + 3]);
-      }
+    for (int j = 0; j < 4; ++j) x[j] = __builtin_fmaf(weight, f[j], x[j]);
+  }
+#pragma unroll
+  for (int d = kLanes; d < 64; d <<= 1) {
+    sum += __shfl_xor(sum, d, 64);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] += __shfl_xor(x[j], d, 64);
+  }
+  if (kRowWaves > 1) {
+    if (lane < kLanes) lds_x[wave][lane] = x;
+    if (lane == 0) lds_sum[wave] = sum;
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) {
+      sum += lds_sum[w];
+      x += lds_x[w][lane & (kLanes - 1)];
     }
   }
+  if (!valid) return;
   const float mul = sum > 0.0f ? (512.0f / 127.0f) / sum : 0.0f;
-  if (seg < dim) {
-    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + out_row * dim + seg);
-#pragma unroll
-    for (int i = 0; i < 2 * DC; ++i) dst[i] = f32x2_to_bf16x2(x[2 * i] * mul, x[2 * i + 1] * mul);
-  }
-  if (a.lse && (tid & 15) == 0) a.lse[out_row] = sum > 0.0f ? (__log2f(sum) + top - 14.0f) * kLn2 : -INFINITY;
+  if (lane < kLanes && at < dim)
+    *reinterpret_cast<uint2*>(a.out + out_row * dim + at) =
+        make_uint2(f32x2_to_bf16x2(x[0] * mul, x[1] * mul), f32x2_to_bf16x2(x[2] * mul, x[3] * mul));
+  if (a.lse && lane == 0) a.lse[out_row] = sum > 0.0f ? (__log2f(sum) + top - 14.0f) * kLn2 : -INFINITY;
 }
 
 // Rows from which the workgroups of 128 rows take over from those of 16.
@@ -760,7 +852,7 @@ constexpr int64_t kPromptFrom = 64;
 // Workgroups along the keys: enough to fill the chip, none with less than a
 // step per wave.  The split is a number of steps, the same for every sequence
 // of the batch, so a short sequence takes fewer workgroups and not shorter ones.
-constexpr int64_t kTargetBlocks = 2048, kTargetPromptBlocks = 512;
+constexpr int64_t kTargetBlocks = 4096, kTargetPromptBlocks = 512;
 
 struct Plan {
   int tile_rows;
@@ -786,8 +878,13 @@ Plan make_plan(const KvView& kv, int64_t seqs, int64_t max_new, int64_t max_len,
   p.row_tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   p.tiles = seqs * kv.heads * p.row_tiles;
   auto splits_of = [&](int64_t steps, int64_t target) {
-    const int64_t wanted = p.tiles < target ? target / p.tiles : 1, most = (steps + kWaves - 1) / kWaves;
-    return wanted < most ? wanted : most;
+    auto pick = [&](int64_t blocks, int64_t least) {
+      const int64_t wanted = p.tiles < blocks ? blocks / p.tiles : 1, most = (steps + least - 1) / least;
+      return wanted < most ? wanted : most;
+    };
+    if (p.tile_rows != 16) return pick(target, kWaves);
+    const int64_t full = pick(target, 4 * kWaves), few = pick(1024, kWaves);
+    return full > few ? full : few;
   };
   int64_t steps = (max_len + kStep - 1) / kStep;
   const int64_t target = p.tile_rows == 16 ? kTargetBlocks : kTargetPromptBlocks;
@@ -816,7 +913,7 @@ hipError_t launch_attention(const KvView& kv, const KvStep& st, int64_t seqs, in
                             int64_t window, int64_t sinks, uint16_t* out, float* lse, void* workspace, hipStream_t s) {
   const Plan p = make_plan(kv, seqs, max_new, max_len, q_heads, window, sinks);
   const int64_t blocks = (p.tiles + 7) / 8 * 8 * p.splits;
-  if (!grid_fits(blocks, 2 * kThreads) || !grid_fits(p.tiles * (p.tile_rows / 16), kThreads)) return kErrGridTooLarge;
+  if (!grid_fits(blocks, 2 * kThreads) || (p.splits > 1 && !grid_fits(p.tiles * p.tile_rows, kThreads))) return kErrGridTooLarge;
   Attn a;
   a.kv = kv;
   a.st = st;
@@ -849,14 +946,21 @@ hipError_t launch_attention(const KvView& kv, const KvStep& st, int64_t seqs, in
       }
       hipLaunchKernelGGL((k_attn_prompt<DC, 1>), dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
     };
-    const dim3 grid((unsigned)blocks), pieces((unsigned)(p.tiles * (p.tile_rows / 16)));
-    if (p.tile_rows == 16)
-      hipLaunchKernelGGL(k_attn<DC>, grid, dim3(kThreads), 0, s, a);
-    else
+    const dim3 grid((unsigned)blocks);
+    if (p.tile_rows == 16) {
+      if (kv.page_tokens >= kStep)
+        hipLaunchKernelGGL((k_attn<DC, 1>), grid, dim3(kThreads), 0, s, a);
+      else
+        hipLaunchKernelGGL((k_attn<DC, 4>), grid, dim3(kThreads), 0, s, a);
+    } else {
       prompt(p.teams);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits <= 1) return e;
-    hipLaunchKernelGGL(k_attn_join<DC>, pieces, dim3(kThreads), 0, s, a);
+    if (p.splits <= 8)
+      hipLaunchKernelGGL((k_attn_join<DC, 1>), dim3((unsigned)(p.tiles * (p.tile_rows / kWaves))), dim3(kThreads), 0, s, a);
+    else
+      hipLaunchKernelGGL((k_attn_join<DC, kWaves>), dim3((unsigned)(p.tiles * p.tile_rows)), dim3(kThreads), 0, s, a);
     return hipGetLastError();
   };
   if (kv.dim <= 64) return go(std::integral_constant<int, 1>{});
