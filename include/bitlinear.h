@@ -345,7 +345,7 @@ size_t bl_rmsnorm_backward_workspace_bytes(int64_t m, int64_t k);
  *           forward call, or x without a residual).
  *   dr      [m][k] bf16, the gradient that reaches r past the norm, or NULL.
  *   dx      out [m][k] bf16: the gradient of x and of the residual alike; may be dr.
- *   dw      out [k] fp32 (overwritten; zero for m = 0).
+ *   dw      out [k] fp32, 16-byte aligned (overwritten; zero for m = 0).
  * The order of the sums is fixed: equal inputs give equal bits.
  * Errors: BL_ERR_NULL, BL_ERR_SHAPE, BL_ERR_ALIGN, BL_ERR_WORKSPACE, BL_ERR_HIP. */
 bl_status bl_rmsnorm_backward(const float* dn, const uint16_t* r, const float* weight, const uint16_t* dr, int64_t m,

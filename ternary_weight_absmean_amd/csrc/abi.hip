@@ -267,7 +267,7 @@ bl_status bl_rmsnorm_backward(const float* dn, const uint16_t* r, const float* w
   if (m < 0 || m > BL_MAX_M || !valid_k(k) || k > BL_MAX_NORM_K || !(eps >= 0.0f && eps < INFINITY)) return BL_ERR_SHAPE;
   if (!dw || (m > 0 && (!dn || !r || !weight || !dx || !workspace))) return BL_ERR_NULL;
   if (!aligned(dn, 16) || !aligned(r, 16) || !aligned(weight, 16) || !aligned(dr, 16) || !aligned(dx, 16) ||
-      !aligned(dw, 4) || !aligned(workspace, 16))
+      !aligned(dw, 16) || !aligned(workspace, 16))
     return BL_ERR_ALIGN;
   hipStream_t s = (hipStream_t)stream;
   if (m == 0) return from_hip(bl::launch_fill_zero(dw, k, s));  // empty sum

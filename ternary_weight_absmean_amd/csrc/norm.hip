@@ -158,8 +158,6 @@ __global__ __launch_bounds__(T) void k_rmsnorm_quant(const uint4* x, const uint4
 // sums in registers; per row one reduction (sum r^2 and sum dn w r).  The
 // workgroups' sums go to the workspace and a second kernel adds them in a
 // fixed order, so no atomics and the same bits every time.
-constexpr int kBackMaxBlocks = 512;
-
 template <int T, int kC>
 __global__ __launch_bounds__(T) void k_rmsnorm_backward(const uint4* __restrict__ dn, const uint4* __restrict__ r,
                                                         const uint4* __restrict__ w, const uint4* dr, int64_t m, int k8,
@@ -250,25 +248,37 @@ __global__ __launch_bounds__(T) void k_rmsnorm_backward(const uint4* __restrict_
   }
 }
 
-// dw = the workgroups' partial sums, added in order: 16 rows of partials at a
-// time per column, 64 columns per workgroup.
-__global__ __launch_bounds__(1024) void k_rmsnorm_dw(const float* __restrict__ part, int blocks, int64_t k,
-                                                     float* __restrict__ dw) {
-  __shared__ float sums[16][64];
-  const int col = threadIdx.x & 63, slot = threadIdx.x >> 6;
-  const int64_t j = (int64_t)blockIdx.x * 64 + col;  // k is a multiple of 64
-  float s = 0.0f;
-  for (int b = slot; b < blocks; b += 16) s += part[b * k + j];
-  sums[slot][col] = s;
+// dw = the workgroups' partial sums, added in a fixed order: 32 columns per
+// workgroup (128-byte pieces of a row of partials, four columns per thread) and
+// 32 rows at a time, eight loads of a thread in flight.
+constexpr int kDwCols = 32, kDwSlots = 32;
+
+__global__ __launch_bounds__(kDwCols / 4 * kDwSlots) void k_rmsnorm_dw(const float* __restrict__ part, int blocks,
+                                                                       int64_t k, float* __restrict__ dw) {
+  typedef float v4f __attribute__((ext_vector_type(4)));
+  __shared__ v4f sums[kDwSlots][kDwCols / 4];
+  const int quad = threadIdx.x % (kDwCols / 4), slot = threadIdx.x / (kDwCols / 4);
+  const int64_t j = (int64_t)blockIdx.x * kDwCols + quad * 4;  // k is a multiple of 64
+  v4f s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+  for (int b = slot; b < blocks; b += kDwSlots) s += *reinterpret_cast<const v4f*>(part + b * k + j);
+  sums[slot][quad] = s;
   __syncthreads();
   if (slot == 0) {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) s += sums[i][col];
-    dw[j] = s;
+    for (int i = 1; i < kDwSlots; ++i) s += sums[i][quad];
+    *reinterpret_cast<v4f*>(dw + j) = s;
   }
 }
 
-int back_blocks(int64_t m) { return (int)(m < kBackMaxBlocks ? m : kBackMaxBlocks); }
+// Workgroups of the backward kernel: about as many as run at once, since each
+// writes a row of partial sums.  4096 x 8192: 74 us with 512, 78 with 256 and
+// 79 with 1024; 8192 x 640: 18 us with 1024, 23 with 512; 1000 x 28672: 81 us
+// with 256, 93 with 512.
+int back_blocks(int64_t m, int64_t k) {
+  const int64_t most = k <= 2048 ? 1024 : k <= 8192 ? 512 : 256;
+  return (int)(m < most ? m : most);
+}
 
 }  // namespace
 
@@ -285,6 +295,9 @@ hipError_t launch_rmsnorm_quant(const uint16_t* x, const uint16_t* residual, con
     return hipGetLastError();
   };
   using std::integral_constant;
+  // a wave per row for the shortest; more than four chunks per thread for none
+  if (k8 <= 64) return go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  if (k8 <= 128) return go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
   if (k8 <= 256) return go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
   if (k8 <= 512) return go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
   if (k8 <= 1024) return go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
@@ -292,11 +305,11 @@ hipError_t launch_rmsnorm_quant(const uint16_t* x, const uint16_t* residual, con
   return go(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
 }
 
-size_t rmsnorm_backward_workspace_bytes(int64_t m, int64_t k) { return (size_t)back_blocks(m) * (size_t)k * 4; }
+size_t rmsnorm_backward_workspace_bytes(int64_t m, int64_t k) { return (size_t)back_blocks(m, k) * (size_t)k * 4; }
 
 hipError_t launch_rmsnorm_backward(const float* dn, const uint16_t* r, const float* w, const uint16_t* dr, int64_t m,
                                    int64_t k, float eps, uint16_t* dx, float* dw, void* workspace, hipStream_t s) {
-  const int k8 = (int)(k / 8), blocks = back_blocks(m);
+  const int k8 = (int)(k / 8), blocks = back_blocks(m, k);
   float* part = (float*)workspace;
   auto go = [&](auto t, auto c) {
     constexpr int T = decltype(t)::value, kC = decltype(c)::value;
@@ -304,7 +317,11 @@ hipError_t launch_rmsnorm_backward(const float* dn, const uint16_t* r, const flo
                        (const uint4*)r, (const uint4*)w, (const uint4*)dr, m, k8, eps, (uint4*)dx, part);
   };
   using std::integral_constant;
-  if (k8 <= 256)
+  if (k8 <= 64)
+    go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  else if (k8 <= 128)
+    go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  else if (k8 <= 256)
     go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
   else if (k8 <= 512)
     go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
@@ -314,7 +331,7 @@ hipError_t launch_rmsnorm_backward(const float* dn, const uint16_t* r, const flo
     go(integral_constant<int, 512>{}, integral_constant<int, 8>{});
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_rmsnorm_dw, dim3((unsigned)(k / 64)), dim3(1024), 0, s, part, blocks, k, dw);
+  hipLaunchKernelGGL(k_rmsnorm_dw, dim3((unsigned)(k / kDwCols)), dim3(kDwCols / 4 * kDwSlots), 0, s, part, blocks, k, dw);
   return hipGetLastError();
 }
 
