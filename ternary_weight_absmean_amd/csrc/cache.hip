@@ -154,54 +154,54 @@ __device__ __forceinline__ void turn_unit(float (&v)[16], const float (&cs)[8], 
   for (int j = 0; j < 8; ++j) {
     if (kInter) {
       const float a = v[2 * j], b = v[2 * j + 1];
-      v[2 * j] = a * cs[j] - b * sn[j];
-      v[2 * j + 1] = a * sn[j] + b * cs[j];
+      v[2 * j] = __builtin_fmaf(a, cs[j], -(b * sn[j]));
+      v[2 * j + 1] = __builtin_fmaf(a, sn[j], b * cs[j]);
     } else {
       const float a = v[j], b = v[8 + j];
-      v[j] = a * cs[j] - b * sn[j];
-      v[8 + j] = a * sn[j] + b * cs[j];
+      v[j] = __builtin_fmaf(a, cs[j], -(b * sn[j]));
+      v[8 + j] = __builtin_fmaf(a, sn[j], b * cs[j]);
     }
   }
 }
 
 // ---- bl_rope ----
-// One thread per unit of kG heads of a token (unit fastest): the angles are
-// evaluated once per unit and used for all kG heads, whose loads are issued
-// together.
+// One thread per unit of a head (unit fastest, then head, then token).  Several
+// heads per thread would share the angles, but take registers from the waves
+// that hide the loads: 4099 tokens of 72 heads of 128 (151 MB) take 31 us with
+// one head per thread, 34 with two, 37 with four.
 constexpr int kRopeThreads = 256;
 
-template <bool kVec, bool kInter, int kG>
+template <bool kVec, bool kInter>
 __global__ __launch_bounds__(kRopeThreads) void k_rope(const uint16_t* x, int64_t xt, int64_t xh,
                                                        const int32_t* __restrict__ position,
                                                        const float* __restrict__ turns, float magnitude, float sign,
-                                                       Head h, uint32_t items, uint32_t groups, int heads, uint16_t* y,
-                                                       int64_t yt, int64_t yh) {
+                                                       Head h, uint32_t items, uint32_t heads, uint16_t* y, int64_t yt,
+                                                       int64_t yh) {
   const uint32_t item = blockIdx.x * kRopeThreads + threadIdx.x;
   if (item >= items) return;
   const uint32_t rest = item / (uint32_t)h.units;
   const int u = (int)(item - rest * (uint32_t)h.units);
-  const uint32_t token = rest / groups;
-  const int head0 = (int)(rest - token * groups) * kG;
-  float v[kG][16];
-#pragma unroll
-  for (int g = 0; g < kG; ++g)
-    if (head0 + g < heads) load_unit<kVec, kInter>(h, u, x + (int64_t)token * xt + (int64_t)(head0 + g) * xh, v[g]);
+  const uint32_t token = rest / heads;
+  const int64_t head = rest - token * heads;
+  float v[16];
+  load_unit<kVec, kInter>(h, u, x + (int64_t)token * xt + head * xh, v);
   if (u < h.turning) {
     float cs[8], sn[8];
     unit_angles<kVec>(h, u, turns, (float)position[token], magnitude, sign, cs, sn);
-#pragma unroll
-    for (int g = 0; g < kG; ++g) turn_unit<kInter>(v[g], cs, sn);
+    turn_unit<kInter>(v, cs, sn);
   }
-#pragma unroll
-  for (int g = 0; g < kG; ++g)
-    if (head0 + g < heads) store_unit<kVec, kInter>(h, u, y + (int64_t)token * yt + (int64_t)(head0 + g) * yh, v[g]);
+  store_unit<kVec, kInter>(h, u, y + (int64_t)token * yt + head * yh, v);
 }
 
 // ---- bl_kv_append ----
 // Grid: y = sequence; x = (touched page, head, k or v), then blocks that
 // rotate q.  A workgroup owns one page of one head: absmax of the new values
-// (rotated in fp32), then codes.  The first kHold units of a thread stay in
-// registers between the two steps, further ones are read again (from L2).
+// (rotated in fp32), then codes.  A thread's first unit stays in registers
+// between the two steps, further ones are read again (from L2), which costs
+// less than the registers: 5 prompts of up to 1777 tokens (64 + 2 x 8 heads of
+// 128) take 52 us with one unit held, 54 with two; the queries' rotation, most of
+// their bytes, hides the pages' loads and is no faster in a launch of its own
+// (40 + 16 us).
 struct Rows {
   const uint16_t* p;
   int64_t token, head;
@@ -223,7 +223,7 @@ __global__ __launch_bounds__(T) void k_kv_append(KvView kv, KvStep st, Rows k, R
                                                  const float* __restrict__ turns, float magnitude, int page_blocks,
                                                  Rows q, int q_heads, uint16_t* q_out) {
   __shared__ float part[T / 64];
-  constexpr int kHold = 2;
+  constexpr int kHold = 1;
   const int s = blockIdx.y, tid = threadIdx.x;
   const int begin = st.begin(s), count = st.count(s, begin), start = st.start_of(s);
   int b = blockIdx.x;
@@ -379,26 +379,18 @@ hipError_t launch_rope(const uint16_t* x, int64_t xt, int64_t xh, const int32_t*
                        int64_t yt, int64_t yh, hipStream_t s) {
   const Head h = make_head(dim, rot);
   const float sign = inverse ? -1.0f : 1.0f;
-  auto go = [&](auto vec, auto inter, auto g) {
-    constexpr bool kVec = decltype(vec)::value, kInter = decltype(inter)::value;
-    constexpr int kG = decltype(g)::value;
-    const int groups = (heads + kG - 1) / kG;
-    const int64_t items = tokens * groups * h.units, blocks = (items + kRopeThreads - 1) / kRopeThreads;
-    if (!grid_fits(blocks, kRopeThreads)) return kErrGridTooLarge;
-    hipLaunchKernelGGL((k_rope<kVec, kInter, kG>), dim3((unsigned)blocks), dim3(kRopeThreads), 0, s, x, xt, xh, position, turns,
-                       magnitude, sign, h, (uint32_t)items, (uint32_t)groups, heads, y, yt, yh);
+  const int64_t items = tokens * heads * h.units, blocks = (items + kRopeThreads - 1) / kRopeThreads;
+  if (!grid_fits(blocks, kRopeThreads)) return kErrGridTooLarge;
+  auto go = [&](auto vec, auto inter) {
+    hipLaunchKernelGGL((k_rope<decltype(vec)::value, decltype(inter)::value>), dim3((unsigned)blocks), dim3(kRopeThreads),
+                       0, s, x, xt, xh, position, turns, magnitude, sign, h, (uint32_t)items, (uint32_t)heads, y, yt, yh);
     return hipGetLastError();
   };
   using std::bool_constant;
-  using std::integral_constant;
-  // four heads per thread once one would make more workgroups than a few rounds of the 256 CUs
-  const bool many = tokens * heads * h.units >= (int64_t)1024 * kRopeThreads;
-  auto pick = [&](auto inter) {
-    if (!vector_runs(dim, rot)) return go(bool_constant<false>{}, inter, integral_constant<int, 1>{});
-    return many ? go(bool_constant<true>{}, inter, integral_constant<int, 4>{})
-                : go(bool_constant<true>{}, inter, integral_constant<int, 1>{});
+  auto by_layout = [&](auto vec) {
+    return interleaved ? go(vec, bool_constant<true>{}) : go(vec, bool_constant<false>{});
   };
-  return interleaved ? pick(bool_constant<true>{}) : pick(bool_constant<false>{});
+  return vector_runs(dim, rot) ? by_layout(bool_constant<true>{}) : by_layout(bool_constant<false>{});
 }
 
 hipError_t launch_kv_append(const KvView& kv, const KvStep& st, int64_t seqs, int64_t max_new, const uint16_t* k,
