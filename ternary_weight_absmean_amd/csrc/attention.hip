@@ -846,66 +846,93 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(Attn a) {
   if (a.lse && lane == 0) a.lse[out_row] = sum > 0.0f ? (__log2f(sum) + top - 14.0f) * kLn2 : -INFINITY;
 }
 
-// Rows from which the workgroups of 128 rows take over from those of 16.
-constexpr int64_t kPromptFrom = 64;
-
 // Workgroups along the keys: enough to fill the chip, none with less than a
 // step per wave.  The split is a number of steps, the same for every sequence
 // of the batch, so a short sequence takes fewer workgroups and not shorter ones.
-constexpr int64_t kTargetBlocks = 4096, kTargetPromptBlocks = 512;
+constexpr int64_t kTargetBlocks = 4096, kTargetPromptBlocks = 512, kUnsplit = 16;
 
 struct Plan {
   int tile_rows;
   int64_t row_tiles, tiles;
-  int64_t most_splits;  // of any window
   int splits, per;
   int teams;  // of a workgroup of 128 rows
 };
 
+// Workgroups of 16 rows (k_attn) or of 128 (k_attn_prompt).  The former read
+// and convert the keys and values once per 16 rows, but their four waves share
+// a tile's steps, so that few rows, and many over few keys, are done sooner:
+// 21 x 1200 rows of 64 over up to 600 keys 13 us against 18, 16 x 756 12.8
+// against 22, 5 x 4000 of 128 over 1000 34 against 34; but 28 x 2644 of 128 over
+// 721 keys 60 us against 36, and 64 tokens of 20 heads over 4064 keys 31 against 26.
+bool few_rows(int64_t rows, int64_t lists, int64_t steps, int dim) {
+  const int64_t tiles = lists * ((rows + 15) / 16), chunks = (dim + 63) / 64;
+  return rows < 64 || (steps <= 32 && tiles * steps * chunks < 40000);
+}
+
 // Two teams (one workgroup of eight waves to a CU) while the tiles fill the
-// 256 CUs less than twice and each has many steps: a tile then takes half the
-// time (376 tiles of up to 94 steps: 133 us against 185 with one team, 256 of 47:
-// 68 against 79, 480 of 103: 182 against 207).  One team (two independent
+// 256 CUs less than twice and have many steps: a tile then takes half the
+// time (376 tiles of up to 94 steps: 133 us against 185 with one team, 256 of
+// 47: 68 against 79, 40 of 16: 34 against 42).  One team (two independent
 // workgroups to a CU) where there are tiles enough (940 of up to 94: 290 us
-// against 302) or few steps (480 of 20: 65 against 73, 96 of 7: 21 against 26).
-bool two_teams(int dim, int64_t tiles, int64_t steps) { return dim <= 128 && tiles < 512 && steps > 24; }
+// against 302) or, past one per CU, few steps (480 of 20: 65 against 73).
+bool two_teams(int dim, int64_t tiles, int64_t steps) {
+  return dim <= 128 && ((tiles < 256 && steps > 6) || (tiles < 512 && steps > 24));
+}
 
 Plan make_plan(const KvView& kv, int64_t seqs, int64_t max_new, int64_t max_len, int64_t q_heads, int64_t window,
                int64_t sinks) {
   Plan p;
-  const int64_t rows = max_new * (q_heads / kv.heads);
-  p.tile_rows = rows >= kPromptFrom ? kPromptRows : 16;
-  p.row_tiles = (rows + p.tile_rows - 1) / p.tile_rows;
-  p.tiles = seqs * kv.heads * p.row_tiles;
-  auto splits_of = [&](int64_t steps, int64_t target) {
-    auto pick = [&](int64_t blocks, int64_t least) {
-      const int64_t wanted = p.tiles < blocks ? blocks / p.tiles : 1, most = (steps + least - 1) / least;
-      return wanted < most ? wanted : most;
-    };
-    if (p.tile_rows != 16) return pick(target, kWaves);
-    const int64_t full = pick(target, 4 * kWaves), few = pick(1024, kWaves);
-    return full > few ? full : few;
+  const int64_t rows = max_new * (q_heads / kv.heads), lists = seqs * kv.heads;
+  auto steps_of = [&](int64_t tile_rows) {
+    const int64_t all = (max_len + kStep - 1) / kStep;
+    if (window <= 0) return all;
+    const int64_t tokens = tile_rows * kv.heads / q_heads + 2;  // that a tile spans
+    const int64_t most = (window + tokens) / kStep + 2 + (sinks + kStep - 1) / kStep;
+    return most < all ? most : all;
   };
-  int64_t steps = (max_len + kStep - 1) / kStep;
-  const int64_t target = p.tile_rows == 16 ? kTargetBlocks : kTargetPromptBlocks;
-  p.most_splits = splits_of(steps, target);
-  if (window > 0) {
-    const int64_t most = (window + p.tile_rows + kStep) / kStep + 1 + (sinks + kStep - 1) / kStep;
-    if (most < steps) steps = most;
-  }
+  p.tile_rows = few_rows(rows, lists, steps_of(kPromptRows), kv.dim) ? 16 : kPromptRows;
+  const int64_t steps = steps_of(p.tile_rows);
+  p.row_tiles = (rows + p.tile_rows - 1) / p.tile_rows;
+  p.tiles = lists * p.row_tiles;
   p.teams = p.tile_rows != 16 && two_teams(kv.dim, p.tiles, steps) ? 2 : 1;
-  const int64_t splits = splits_of(steps, target / p.teams);
+  auto pick = [&](int64_t blocks, int64_t least) {
+    const int64_t wanted = p.tiles < blocks ? blocks / p.tiles : 1, most = (steps + least - 1) / least;
+    return wanted < most ? wanted : most;
+  };
+  int64_t splits = 1;
+  if (steps <= kUnsplit) {
+    // the join and its launch would take longer
+  } else if (p.tile_rows == 16) {
+    const int64_t full = pick(kTargetBlocks, 4 * kWaves), few = pick(1024, kWaves);
+    splits = full > few ? full : few;
+  } else {
+    splits = pick(kTargetPromptBlocks / p.teams, kWaves);
+  }
   p.per = (int)((steps + splits - 1) / splits);
-  p.splits = (int)((steps + p.per - 1) / p.per);  // at most splits, so at most most_splits
+  p.splits = (int)((steps + p.per - 1) / p.per);
   return p;
+}
+
+// The most splits that any window of these sizes takes: with fewer steps the
+// tiles may be of 16 rows instead of 128, and of either there are never more
+// splits than these.
+int64_t most_splits(const KvView& kv, int64_t seqs, int64_t max_new, int64_t max_len, int64_t q_heads) {
+  const int64_t rows = max_new * (q_heads / kv.heads), steps = (max_len + kStep - 1) / kStep;
+  auto most = [&](int64_t tile_rows, int64_t target) {
+    const int64_t tiles = seqs * kv.heads * ((rows + tile_rows - 1) / tile_rows);
+    const int64_t wanted = tiles < target ? target / tiles : 1, limit = (steps + kWaves - 1) / kWaves;
+    return wanted < limit ? wanted : limit;
+  };
+  const int64_t a = most(16, kTargetBlocks), b = rows < 64 ? 1 : most(kPromptRows, kTargetPromptBlocks);
+  return a > b ? a : b;
 }
 
 }  // namespace
 
 size_t attention_workspace_bytes(const KvView& kv, int64_t seqs, int64_t tokens, int64_t max_new, int64_t max_len,
                                  int64_t q_heads) {
-  const Plan p = make_plan(kv, seqs, max_new, max_len, q_heads, 0, 0);
-  return p.most_splits <= 1 ? 0 : (size_t)tokens * (size_t)q_heads * (size_t)p.most_splits * (size_t)(kv.dim + 2) * 4;
+  const int64_t splits = most_splits(kv, seqs, max_new, max_len, q_heads);
+  return splits <= 1 ? 0 : (size_t)tokens * (size_t)q_heads * (size_t)splits * (size_t)(kv.dim + 2) * 4;
 }
 
 hipError_t launch_attention(const KvView& kv, const KvStep& st, int64_t seqs, int64_t tokens, int64_t max_new,
