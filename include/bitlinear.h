@@ -289,6 +289,8 @@ size_t bl_backward_w_workspace_bytes(int64_t m, int64_t n, int64_t k);
 /* Weight gradient for the shadow weights: dw[j][t] = sum_i dy[i][j] *
  * alpha[i] * xq[i][t] / 127.  alpha[i] * dy[i][j] (two bf16 values) is split
  * exactly into two bf16 parts, so every product is exact; the sums are fp32.
+ * An alpha with more bits than bf16's (bl_rmsnorm_quant writes such) is taken
+ * too: the two parts then hold each product to 2^-17 of it.
  *   dy         [m][n] bf16 bit patterns; xq [m][k] int8 and alpha [m] fp32 as
  *              written by bl_quant_act / bl_bitlinear for the layer's input.
  *   dw         out [n][k] fp32 (overwritten; zero for m = 0).
@@ -317,7 +319,8 @@ bl_status bl_unpack_ternary(const uint8_t* packed, int64_t n, int64_t k, int8_t*
  *   alpha = max_j |n_j|,  s = fl32(127 / max(alpha, 1e-5f)),
  *   xq = round_half_even(fl32(n * s)),
  *   y = bf16(n),   xhat = bf16(xq * fl32(alpha / 127)).
- * The norm and its codes are those of the fp32 sum, not of the rounded r.
+ * The norm and its codes are those of the fp32 sum, not of the rounded r;
+ * alpha is the fp32 maximum (bl_quant_act's is a bf16 value, as its input is).
  *   x, residual  [m][k] bf16; residual may be NULL.
  *   weight       [k] fp32.   eps finite, >= 0.
  *   r, y, xhat   out [m][k] bf16, each NULL to skip it; r may be x or residual.

@@ -30,8 +30,8 @@
 // The weight gradient dw[j][t] = sum_i alpha_i dy[i][j] xq[i][t] / 127
 // contracts over the tokens, the row index of both inputs, so a preparation
 // kernel first writes them token-contiguous into the caller's workspace:
-// a = alpha_i * dy[i][j] (a product of two bf16 values: 16 significant bits,
-// exact in fp32) split into a_hi = bf16(a) and a_lo = a - a_hi (at most 8
+// a = alpha_i * dy[i][j] (of two bf16 values: 16 significant bits, exact in
+// fp32; an fp32 alpha is taken too, a_hi + a_lo then being right to 2^-17) split into a_hi = bf16(a) and a_lo = a - a_hi (at most 8
 // significant bits: exact in bf16), transposed to [n][m_pad]; and xq
 // converted to bf16 (exact) and transposed to [k][m_pad]; tokens past m are
 // zero.  k_bwd_w then runs two bf16 MFMAs per tile pair (a_hi and a_lo with
@@ -249,9 +249,9 @@ __global__ __launch_bounds__(256) void k_bwd_w_prep(const uint16_t* __restrict__
     for (int e = 0; e < 16; ++e) {
       uint16_t h = 0, l = 0;
       if (i < m) {
-        const float a = __uint_as_float((uint32_t)dy[i * n + c0 + cc + e] << 16) * al;  // exact
+        const float a = __uint_as_float((uint32_t)dy[i * n + c0 + cc + e] << 16) * al;
         h = f32_to_bf16_rne(a);
-        l = (uint16_t)(__float_as_uint(a - __uint_as_float((uint32_t)h << 16)) >> 16);  // exact
+        l = f32_to_bf16_rne(a - __uint_as_float((uint32_t)h << 16));  // exact for a bf16 alpha
       }
       hi_s[rr][cc + e] = h;
       lo_s[rr][cc + e] = l;
