@@ -471,7 +471,7 @@ __global__ __launch_bounds__(kThreads, DC == 1 ? 4 : DC == 2 ? (kPages == 1 ? 3 
 // ---- many rows ----
 // One workgroup: 128 query rows (tokens times the heads of a group) of one
 // sequence and cache head, 32 rows per wave, over the steps of one split.  Keys
-// and values of a step (64 tokens) go through LDS, in three buffers: wave w
+// and values of a step (64 tokens) go through LDS, in two buffers: wave w
 // stages tokens 16w .. 16w + 15 while it computes on the step before, K as it
 // is and V already as fp16, so each value is converted once per 128 rows.
 // One team of four waves takes all steps, two workgroups to a CU; or two teams
@@ -486,7 +486,7 @@ typedef int v16i __attribute__((ext_vector_type(16)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr int kPromptRows = 128;
-constexpr int kRing = 3;
+constexpr int kRing = 2;
 
 template <int DC>
 __device__ __forceinline__ int k_key(int m) {
@@ -559,6 +559,13 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
   vpiece v_raw[8];
   float ka_raw = 0.0f, va_raw = 0.0f;
   bool there = false;
+  uint32_t koff[DC];  // lane offsets beside wave-uniform addresses
+#pragma unroll
+  for (int i = 0; i < DC; ++i) {
+    const int unit = lane + 64 * i, tok = unit / (4 * DC), c = unit % (4 * DC);
+    koff[i] = (uint32_t)(tok * dim + (16 * c < dim ? 16 * c : 0));
+  }
+  const uint32_t voff = (uint32_t)(4 * g * dim + (2 * DC * col < dim ? 2 * DC * col : 0));
   auto page_of = [&](int step) -> int64_t {
     if (step >= s1) return -1;
     const int key = t.key0(step) + 16 * wave;
@@ -572,14 +579,11 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
     ka_raw = a.kv.k_absmax[block];
     va_raw = a.kv.v_absmax[block];
     const int8_t* kp = a.kv.k + at;
-    const int8_t* vp = a.kv.v + at + (4 * g) * dim + (2 * DC * col < dim ? 2 * DC * col : 0);
+    const int8_t* vp = a.kv.v + at;
 #pragma unroll
-    for (int i = 0; i < DC; ++i) {
-      const int unit = lane + 64 * i, tok = unit / (4 * DC), c = unit % (4 * DC);
-      k_raw[i] = *reinterpret_cast<const v4i*>(kp + tok * dim + (16 * c < dim ? 16 * c : 0));
-    }
+    for (int i = 0; i < DC; ++i) k_raw[i] = *reinterpret_cast<const v4i*>(kp + koff[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v_raw[j] = *reinterpret_cast<const vpiece*>(vp + (8 * (j >> 2) + (j & 3)) * dim);
+    for (int j = 0; j < 8; ++j) v_raw[j] = *reinterpret_cast<const vpiece*>(vp + (8 * (j >> 2) + (j & 3)) * dim + voff);
   };
   auto store = [&](int buf) {
 #pragma unroll
@@ -604,44 +608,46 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
     }
   };
 
-  // products of the two 32-key halves of a step; heads past 128 elements have
-  // no registers left to hold one half's while the other's are made
-  constexpr bool kAhead = DC <= 2;
-  v16i high[2], lo[2];
-  auto product = [&](int buf, int h) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) high[h][j] = 0, lo[h][j] = 0;
-    const int tok = 32 * h + col;
-#pragma unroll
-    for (int c = 0; c < kTiles; ++c) {
-      const v4i kf = ring.k[buf][tok * 4 * DC + ((2 * c + g) ^ k_key<DC>(tok))];
-      high[h] = __builtin_amdgcn_mfma_i32_32x32x32_i8(kf, qhi[c], high[h], 0, 0, 0);
-      lo[h] = __builtin_amdgcn_mfma_i32_32x32x32_i8(kf, qlo[c], lo[h], 0, 0, 0);
-    }
-  };
-  // Wave priorities: staging before the products before the exponentials, so
-  // that of the two waves of a SIMD the one that others wait for, or that feeds
-  // the matrix cores, goes first (6000 tokens, 20/5 heads: 290 us without, 269
-  // with; staging alone or the other order 268 to 286).
-  // half h of the step in buffer buf; the products of the following half (of
-  // buffer next) are issued among its vector instructions
-  auto half = [&](int step, int buf, auto which, int next) {
-    constexpr int h = decltype(which)::value;
-    const int j0 = t.key0(step);
+  // Half h (32 keys) of the step in buffer buf.  Wave priorities: staging before
+  // the products before the exponentials, so that of the two waves of a SIMD the
+  // one that others wait for, or that feeds the matrix cores, goes first (6000
+  // tokens, 20/5 heads: 290 us without, 269 with; staging alone or the other
+  // order 268 to 286).
+  auto half = [&](int step, int buf, int h) {
+    const int j0 = t.key0(step), tok = 32 * h + col;
     const float4 sc[2] = {ring.scale[buf][2 * h], ring.scale[buf][2 * h + 1]};
     // wave-uniform: whether all of its rows see all of the half
     const bool all = j0 + 32 * h + 32 <= min(first_pos + 1, t.keys) &&
                      (a.window == 0 || j0 + 32 * h > last_pos - a.window || j0 + 32 * h + 32 <= a.sinks) &&
                      __builtin_amdgcn_readfirstlane(sc[0].w * sc[1].w != 0.0f);
-    float x[16], top;
     __builtin_amdgcn_s_setprio(1);
-    product(kAhead ? next : buf, kAhead ? h ^ 1 : h);
+    v16i high, lo;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) high[j] = lo[j] = 0;
+#pragma unroll
+    for (int c = 0; c < kTiles; ++c) {
+      const v4i kf = ring.k[buf][tok * 4 * DC + ((2 * c + g) ^ k_key<DC>(tok))];
+      high = __builtin_amdgcn_mfma_i32_32x32x32_i8(kf, qhi[c], high, 0, 0, 0);
+      lo = __builtin_amdgcn_mfma_i32_32x32x32_i8(kf, qlo[c], lo, 0, 0, 0);
+    }
+    // the values' operands on their way before the softmax begins (heads past
+    // 128 elements have no registers left for that)
+    uint4 vf[2][kTiles];
+    auto read_v = [&](int b) {
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) vf[b][i] = ring.v[buf][((2 * h + b) * kTiles + i) * 64 + lane];
+    };
+    if (DC <= 2) {
+      read_v(0);
+      read_v(1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    float x[16], top = kNone;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const float mul = row_scale * sc[b].x, add = sc[b].y + (14.0f - m);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        x[8 * b + j] = __builtin_fmaf((float)(high[h][8 * b + j] * 256 + lo[h][8 * b + j]), mul, add);
+      for (int j = 0; j < 8; ++j) x[8 * b + j] = __builtin_fmaf((float)(high[8 * b + j] * 256 + lo[8 * b + j]), mul, add);
     }
     if (!all) {
       asm volatile("; masked keys");  // stays a branch: most steps need none of this
@@ -653,7 +659,6 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
         x[j] = seen ? x[j] : -INFINITY;
       }
     }
-    top = kNone;
 #pragma unroll
     for (int j = 0; j < 16; ++j) top = fmaxf(top, x[j]);
     top = halves_max(top);
@@ -676,6 +681,7 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
     __builtin_amdgcn_s_setprio(0);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
+      if (DC > 2) read_v(b);
       v8h pf;
       float sum = 0.0f;
 #pragma unroll
@@ -686,17 +692,14 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
       }
       l = __builtin_fmaf(sum, sc[b].z, l);
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        const uint4 raw = ring.v[buf][((2 * h + b) * kTiles + i) * 64 + lane];
-        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, raw), pf, o[i], 0, 0, 0);
-      }
+      for (int i = 0; i < kTiles; ++i)
+        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, vf[b][i]), pf, o[i], 0, 0, 0);
     }
   };
 
-  // A team's step is staged while the first half of the one before is worked
-  // on, behind one barrier per step: a wave that stores the n-th has passed the
-  // barrier in the (n - 2)-th, so every wave is done with the (n - 3)-th, whose
-  // buffer (of three) it takes.
+  // A team's step is staged while the one before is worked on, behind one
+  // barrier per step: a wave that stores the n-th has passed the barrier after
+  // the (n - 2)-th, whose buffer it takes.
   constexpr int kStride = kTeams;
   const int rounds = (s1 - s0 + kStride - 1) / kStride;
   int step = s0 + team, buf = 0;
@@ -711,29 +714,30 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
     next_page = page_of(step + 2 * kStride);
   }
   __syncthreads();
-  if (kAhead && busy && step < s1) product(0, 0);
-  for (int round = 0; round < rounds; ++round, step += kStride) {
-    const int next = buf == kRing - 1 ? 0 : buf + 1;
+  for (int round = 0; round < rounds; ++round, step += kStride, buf ^= 1) {
     const bool mine = busy && step < s1;
-    if (mine) half(step, buf, std::integral_constant<int, 0>{}, buf);
+    if (mine) half(step, buf, 0);
     __builtin_amdgcn_s_setprio(3);
-    if (step + kStride < s1) store(next);
-    __syncthreads();
+    if (step + kStride < s1) store(buf ^ 1);
     if (step + 2 * kStride < s1) {
       load(step + 2 * kStride, next_page);
       next_page = page_of(step + 3 * kStride);
     }
-    // (after the last step the products of a stale buffer are not used)
-    if (mine) half(step, buf, std::integral_constant<int, 1>{}, next);
-    buf = next;
+    if (mine) half(step, buf, 1);
+    __syncthreads();
   }
 
   l += __shfl_xor(l, 32, 64);
   if (kTeams == 2) {
     // the second team's rows meet the first's, lane by lane
-    float4* out = reinterpret_cast<float4*>(&rings[1].v[0][0]) + wave * 4 * kTiles * 64 + lane;
-    float2* out_ml = reinterpret_cast<float2*>(&rings[0].v[0][0]) + wave * 64 + lane;
-    __syncthreads();
+    struct Meeting {  // over both teams' buffers, which nobody reads any more
+      float4 o[4][4 * kTiles][64];
+      float2 ml[4][64];
+    };
+    static_assert(kTeams == 1 || sizeof(Meeting) <= sizeof(rings), "the teams meet in their buffers");
+    Meeting& meeting = *reinterpret_cast<Meeting*>(&rings);
+    float4* out = &meeting.o[wave][0][lane];
+    float2* out_ml = &meeting.ml[wave][lane];
     if (team == 1) {
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
