@@ -99,12 +99,15 @@ __device__ __forceinline__ bool find_tile(const Attn& a, int index, Tile& t) {
   const int rt = index - rest * a.row_tiles;
   t.seq = rest / a.kv.heads;
   t.head = rest - t.seq * a.kv.heads;
-  t.begin = a.st.begin(t.seq);
-  const int count = a.st.count(t.seq, t.begin);
+  const KvStep& st = a.st;  // the three integers in one round trip
+  const int from = uniform_load(st.offsets + t.seq), to = uniform_load(st.offsets + t.seq + 1);
+  const int start = uniform_load(st.start + t.seq);
+  t.begin = st.begin_of(from);
+  const int count = st.count_of(t.begin, to);
   t.rows = count * a.group;
   t.row0 = rt * a.tile_rows;
   if (t.row0 >= t.rows) return false;
-  t.start = a.st.start_of(t.seq);
+  t.start = st.start_from(start);
   t.first_pos = t.start + t.row0 / a.group;
   t.last_pos = t.start + (min(t.row0 + a.tile_rows, t.rows) - 1) / a.group;
   const int64_t room = a.st.table_stride << a.page_shift;

@@ -117,9 +117,12 @@ struct KvStep {
   const int32_t *page_table, *start, *offsets;
   int64_t table_stride;
   int tokens, max_new;
-  __device__ int begin(int s) const { return min(max(offsets[s], 0), tokens); }
-  __device__ int count(int s, int begin) const { return min(min(max(offsets[s + 1], begin), tokens) - begin, max_new); }
-  __device__ int start_of(int s) const { return min(max(start[s], 0), 1 << 29); }
+  __device__ int begin_of(int from) const { return min(max(from, 0), tokens); }
+  __device__ int count_of(int begin, int to) const { return min(min(max(to, begin), tokens) - begin, max_new); }
+  __device__ static int start_from(int start) { return min(max(start, 0), 1 << 29); }
+  __device__ int begin(int s) const { return begin_of(offsets[s]); }
+  __device__ int count(int s, int begin) const { return count_of(begin, offsets[s + 1]); }
+  __device__ int start_of(int s) const { return start_from(start[s]); }
   __device__ int64_t page(int s, int64_t index) const { return page_table[s * table_stride + index]; }
 };
 
