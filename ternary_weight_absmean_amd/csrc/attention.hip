@@ -221,12 +221,16 @@ constexpr float kSlack = 1.5f;
 // straight into registers; the next step's keys are asked for as soon as the
 // products have read this step's, its values as soon as those are converted, so
 // that loads are in flight nearly all the time without a second set of
-// registers.  kPages: pages that 64 tokens lie in (1, or 4 for pages of 16 and
+// registers (three waves per SIMD, 16 KB in flight each).  HBM-bound: 24
+// sequences of up to 32768 tokens, 64/8 heads of 128 (883 MB): 160 us, 5.5 TB/s,
+// and 9 us for the join; one token over 1500 (20/5 heads): 7.6 + 4 us, the
+// chain of page number, keys, products, meeting of the waves, join.
+// kPages: pages that 64 tokens lie in (1, or 4 for pages of 16 and
 // 32 tokens, looked up for each 16 tokens).
 template <int DC, int kPages>
 __global__ __launch_bounds__(kThreads, DC == 1 ? 4 : DC == 2 ? (kPages == 1 ? 3 : 2) : 1) void k_attn(Attn a) {
   typedef typename VBytes<DC>::type vbytes;
-  __shared__ float lds_o[kWaves][16][64 * DC];
+  __shared__ float lds_o[kWaves][16][64 * DC + 4];  // rows four banks apart
   __shared__ float lds_ml[kWaves][16][2];
   int index, split;
   if (!tile_and_split(a, index, split)) return;
@@ -477,6 +481,12 @@ __global__ __launch_bounds__(kThreads, DC == 1 ? 4 : DC == 2 ? (kPages == 1 ? 3 
 // and values of a step (64 tokens) go through LDS, in two buffers: wave w
 // stages tokens 16w .. 16w + 15 while it computes on the step before, K as it
 // is and V already as fp16, so each value is converted once per 128 rows.
+// Bound by vector instructions: per 64 keys a wave issues about 330 of them,
+// 32 of which (the exponentials) take four turns, against 32 MFMAs of 32 cycles;
+// with two waves per SIMD the vector pipe is busy for two thirds of the time.
+// 24000 tokens of 20/5 heads of 128: 850 TFLOP/s (a bf16 library product of 8192
+// cubed reaches 1217); 6000 tokens: 252 us, 730 TFLOP/s, where the longest tiles
+// (94 steps) set the end.
 // One team of four waves takes all steps, two workgroups to a CU; or two teams
 // take them in turn, each with its own running state and buffers, one workgroup
 // to a CU, and are joined in LDS at the end (see make_plan for which).

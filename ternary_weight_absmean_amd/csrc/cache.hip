@@ -18,11 +18,15 @@ namespace bl {
 namespace {
 
 // One thread's unit of a head: 16 elements as two runs of eight.  Units
-// 0 .. R-1 (R = ceil(rot / 16)) hold eight pairs each, the rest copy:
-//   halves:      runs at 8u and rot/2 + 8u, pairs (run 0 [j], run 1 [j]);
-//   interleaved: runs at 16u and 16u + 8, neighbouring pairs;
-//   past rot:    runs at rot + 16(u - R) and 8 further.
-// A thread owns its unit's elements, so a rotation in place is safe.
+// 0 .. R-1 (R = ceil(rot / 16)) hold eight pairs each, the rest copy.  Where
+// runs are whole 16-byte pieces (kVec), neighbouring units' runs lie side by
+// side, so that a wave's loads and stores cover whole lines:
+//   turned: runs at 8u and rot/2 + 8u; pairs are (run 0 [j], run 1 [j]) or, for
+//           neighbouring elements (kInter), those inside a run;
+//   copied: runs at rot + 8(u - R) and as many units further.
+// Otherwise the runs of a turned unit are at 8u and rot/2 + 8u, or 16u and
+// 16u + 8, and those of a copied one at rot + 16(u - R) and 8 further, element
+// by element.  A thread owns its unit's elements, so a rotation in place is safe.
 struct Head {
   int dim, rot, half, turning, units;  // turning = R
 };
@@ -40,25 +44,24 @@ __host__ __device__ inline Head make_head(int dim, int rot) {
 // Runs are whole, 8-element-aligned 16-byte pieces (a copied unit may lack its second).
 inline bool vector_runs(int dim, int rot) { return rot % 16 == 0 && dim % 8 == 0; }
 
-// Template arguments below: kVec, all runs are whole; kInter, neighbouring pairs.
-
 // First element of run `run` of unit u, and one past the last the unit may touch there.
-template <bool kInter>
+template <bool kVec, bool kInter>
 __device__ __forceinline__ int run_start(const Head& h, int u, int run) {
-  if (u >= h.turning) return h.rot + 16 * (u - h.turning) + 8 * run;
-  return kInter ? 16 * u + 8 * run : 8 * u + (run ? h.half : 0);
+  if (u >= h.turning)
+    return kVec ? h.rot + 8 * (u - h.turning + run * (h.units - h.turning)) : h.rot + 16 * (u - h.turning) + 8 * run;
+  return !kVec && kInter ? 16 * u + 8 * run : 8 * u + (run ? h.half : 0);
 }
-template <bool kInter>
+template <bool kVec, bool kInter>
 __device__ __forceinline__ int run_limit(const Head& h, int u, int run) {
   if (u >= h.turning) return h.dim;
-  return kInter || run ? h.rot : h.half;
+  return (!kVec && kInter) || run ? h.rot : h.half;
 }
 
 template <bool kVec, bool kInter>
 __device__ __forceinline__ void load_unit(const Head& h, int u, const uint16_t* row, float (&v)[16]) {
 #pragma unroll
   for (int run = 0; run < 2; ++run) {
-    const int at = run_start<kInter>(h, u, run), limit = run_limit<kInter>(h, u, run);
+    const int at = run_start<kVec, kInter>(h, u, run), limit = run_limit<kVec, kInter>(h, u, run);
     if (kVec) {
       uint4 d = make_uint4(0, 0, 0, 0);
       if (at < limit) d = *reinterpret_cast<const uint4*>(row + at);
@@ -81,7 +84,7 @@ template <bool kVec, bool kInter, bool kPast>
 __device__ __forceinline__ void store_unit(const Head& h, int u, uint16_t* row, const float (&v)[16]) {
 #pragma unroll
   for (int run = 0; run < 2; ++run) {
-    const int at = run_start<kInter>(h, u, run), limit = run_limit<kInter>(h, u, run);
+    const int at = run_start<kVec, kInter>(h, u, run), limit = run_limit<kVec, kInter>(h, u, run);
     if (kVec) {
       typedef unsigned v4u __attribute__((ext_vector_type(4)));
       const v4u w = {f32x2_to_bf16x2(v[8 * run], v[8 * run + 1]), f32x2_to_bf16x2(v[8 * run + 2], v[8 * run + 3]),
@@ -104,7 +107,7 @@ template <bool kVec, bool kInter>
 __device__ __forceinline__ void store_codes(const Head& h, int u, int8_t* row, const float (&v)[16], float s) {
 #pragma unroll
   for (int run = 0; run < 2; ++run) {
-    const int at = run_start<kInter>(h, u, run), limit = run_limit<kInter>(h, u, run);
+    const int at = run_start<kVec, kInter>(h, u, run), limit = run_limit<kVec, kInter>(h, u, run);
     uint32_t c[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) c[j] = __float_as_uint(v[8 * run + j] * s + 12582912.0f);
@@ -125,15 +128,16 @@ __device__ __forceinline__ void store_codes(const Head& h, int u, int8_t* row, c
 
 // cos and sin (times the magnitude; sin negated for the inverse) of the eight
 // pairs of unit u at position pos.
-template <bool kVec>
+template <bool kVec, bool kInter>
 __device__ __forceinline__ void unit_angles(const Head& h, int u, const float* turns, float pos, float magnitude,
                                             float sign, float (&cs)[8], float (&sn)[8]) {
   float f[16];
   if (kVec) {
-    const float4* t = reinterpret_cast<const float4*>(turns) + 4 * u;
+    // two pairs per 16 bytes: eight pairs from 8u on, or four from 4u and four from rot/4 + 4u
+    const float4* t = reinterpret_cast<const float4*>(turns) + (kInter ? 2 : 4) * u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 q = t[i];
+      const float4 q = t[kInter && i >= 2 ? h.half / 4 + i - 2 : i];
       f[4 * i] = q.x, f[4 * i + 1] = q.y, f[4 * i + 2] = q.z, f[4 * i + 3] = q.w;
     }
   } else {
@@ -194,7 +198,7 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(const uint16_t* x, int64_
   load_unit<kVec, kInter>(h, u, x + (int64_t)token * xt + head * xh, v);
   if (u < h.turning) {
     float cs[8], sn[8];
-    unit_angles<kVec>(h, u, turns, (float)position[token], magnitude, sign, cs, sn);
+    unit_angles<kVec, kInter>(h, u, turns, (float)position[token], magnitude, sign, cs, sn);
     turn_unit<kInter>(v, cs, sn);
   }
   store_unit<kVec, kInter, true>(h, u, y + (int64_t)token * yt + head * yh, v);
@@ -206,9 +210,13 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(const uint16_t* x, int64_
 // (rotated in fp32), then codes.  A thread's first unit stays in registers
 // between the two steps, further ones are read again (from L2), which costs
 // less than the registers: 5 prompts of up to 1777 tokens (64 + 2 x 8 heads of
-// 128) take 52 us with one unit held, 54 with two; the queries' rotation, most of
-// their bytes, hides the pages' loads and is no faster in a launch of its own
-// (40 + 16 us).
+// 128, 227 MB) take 50 us (4.5 TB/s) with one unit held, 52 with two; the
+// queries' rotation, most of their bytes, hides the pages' loads and is no
+// faster in a launch of its own (40 + 16 us).  64 sequences' single tokens of
+// 20 + 2 x 5 heads take 4 us, a launch and its dependent loads (page number,
+// absmax).  A prompt's queries are stored past the caches like k_rope's outputs
+// (61 us against 63 with the read back; the decoder example's pass is the
+// same), a decoded token's are left in them for the attention.
 struct Rows {
   const uint16_t* p;
   int64_t token, head;
@@ -245,10 +253,10 @@ __global__ __launch_bounds__(T) void k_kv_append(KvView kv, KvStep st, Rows k, R
     load_unit<kVec, kInter>(kh, u, q.p + token * q.token + head * q.head, x);
     if (u < kh.turning) {
       float cs[8], sn[8];
-      unit_angles<kVec>(kh, u, turns, (float)((int64_t)start + i), magnitude, 1.0f, cs, sn);
+      unit_angles<kVec, kInter>(kh, u, turns, (float)((int64_t)start + i), magnitude, 1.0f, cs, sn);
       turn_unit<kInter>(x, cs, sn);
     }
-    store_unit<kVec, kInter, false>(kh, u, q_out + (token * q_heads + head) * kh.dim, x);
+    store_unit<kVec, kInter, T != 64>(kh, u, q_out + (token * q_heads + head) * kh.dim, x);
     return;
   }
   const bool is_v = b & 1;
@@ -285,7 +293,7 @@ __global__ __launch_bounds__(T) void k_kv_append(KvView kv, KvStep st, Rows k, R
     load_unit<kVec, kInter>(h, u, from, x);
     if (u < h.turning) {
       float cs[8], sn[8];
-      unit_angles<kVec>(h, u, turns, (float)(first + keep + row), magnitude, 1.0f, cs, sn);
+      unit_angles<kVec, kInter>(h, u, turns, (float)(first + keep + row), magnitude, 1.0f, cs, sn);
       turn_unit<kInter>(x, cs, sn);
     }
   };
@@ -345,7 +353,8 @@ __global__ __launch_bounds__(T) void k_kv_append(KvView kv, KvStep st, Rows k, R
 }
 
 // ---- bl_kv_read ----
-// One thread per 16 codes of a token's head (chunk fastest); y = sequence, z = k or v.
+// One thread per 16 codes of a token's head (chunk fastest); y = sequence, z = k
+// or v.  36 MB (a third in, two thirds out) in 10 us.
 constexpr int kReadThreads = 256;
 
 __global__ __launch_bounds__(kReadThreads) void k_kv_read(KvView kv, KvStep st, uint16_t* __restrict__ k,

@@ -59,6 +59,8 @@ __device__ __forceinline__ float wave_sum(float v) {
 // One workgroup of T threads per row, kC chunks of eight columns per thread
 // (chunk c of thread t covers columns 8 * (t + c * T)).  Loads go through
 // buffer resources over the row, so chunks past k read as zero and add nothing.
+// 2048 x 8192 with residual, sum and xhat (151 MB): 22.7 us; 1 x 2560: 2.2 us,
+// a launch and its round trips.
 template <int T, int kC>
 __global__ __launch_bounds__(T) void k_rmsnorm_quant(const uint4* x, const uint4* residual, const uint4* __restrict__ w,
                                                      int k8, float eps, uint4* r, uint4* y, uint4* xhat, uint2* xq,
@@ -167,7 +169,10 @@ __global__ __launch_bounds__(T) void k_rmsnorm_quant(const uint4* x, const uint4
 // A workgroup walks over rows (row b, b + grid, ...) and keeps its columns' dw
 // sums in registers; per row one reduction (sum r^2 and sum dn w r).  The
 // workgroups' sums go to the workspace and a second kernel adds them in a
-// fixed order, so no atomics and the same bits every time.
+// fixed order, so no atomics and the same bits every time.  HBM-bound: 4096 x
+// 8192 with dr (336 MB, and 17 MB of partial sums written and read again) 68 +
+// 5 us; 333 x 6912 8.8 + 4.1 us, one row per workgroup, so two round trips and a
+// reduction each.
 template <int T, int kC>
 __global__ __launch_bounds__(T) void k_rmsnorm_backward(const uint4* __restrict__ dn, const uint4* __restrict__ r,
                                                         const uint4* __restrict__ w, const uint4* dr, int64_t m, int k8,
