@@ -554,10 +554,6 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
   const int q_head = t.head * a.group + (valid ? row - token * a.group : 0);
   const int pos = t.start + token, low = a.window > 0 ? pos - a.window + 1 : 0;
   const int first_pos = t.start + wave_row / a.group, last_pos = t.start + (min(wave_row + 32, t.rows) - 1) / a.group;
-  v4i qhi[kTiles], qlo[kTiles];
-  const float row_scale = split_query<32, kTiles>(a.q + (int64_t)(t.begin + token) * a.qt + (int64_t)q_head * a.qh, valid,
-                                                  dim, g, qhi, qlo) *
-                          a.scale * (1.0f / 127.0f);
   v16f o[kTiles];
 #pragma unroll
   for (int i = 0; i < kTiles; ++i)
@@ -620,6 +616,19 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
       ring.scale[buf][wave] = make_float4(ka_raw, __builtin_amdgcn_logf(va), __builtin_amdgcn_rcpf(va), there ? 1.0f : 0.0f);
     }
   };
+
+  // the first step's keys and values travel while the queries are split
+  constexpr int kStride = kTeams;
+  int step = s0 + team, buf = 0;
+  int64_t next_page = page_of(step);
+  if (step < s1) {
+    load(step, next_page);
+    next_page = page_of(step + kStride);
+  }
+  v4i qhi[kTiles], qlo[kTiles];
+  const float row_scale = split_query<32, kTiles>(a.q + (int64_t)(t.begin + token) * a.qt + (int64_t)q_head * a.qh, valid,
+                                                  dim, g, qhi, qlo) *
+                          a.scale * (1.0f / 127.0f);
 
   // Half h (32 keys) of the step in buffer buf.  Wave priorities: staging before
   // the products before the exponentials, so that of the two waves of a SIMD the
@@ -713,15 +722,8 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
   // A team's step is staged while the one before is worked on, behind one
   // barrier per step: a wave that stores the n-th has passed the barrier after
   // the (n - 2)-th, whose buffer it takes.
-  constexpr int kStride = kTeams;
   const int rounds = (s1 - s0 + kStride - 1) / kStride;
-  int step = s0 + team, buf = 0;
-  int64_t next_page = page_of(step);
-  if (step < s1) {
-    load(step, next_page);
-    next_page = page_of(step + kStride);
-    store(0);
-  }
+  if (step < s1) store(0);
   if (step + kStride < s1) {
     load(step + kStride, next_page);
     next_page = page_of(step + 2 * kStride);
