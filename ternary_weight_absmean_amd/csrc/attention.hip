@@ -478,7 +478,7 @@ __global__ __launch_bounds__(kThreads, DC == 1 ? 4 : DC == 2 ? (kPages == 1 ? 3 
 // ---- many rows ----
 // One workgroup: 128 query rows (tokens times the heads of a group) of one
 // sequence and cache head, 32 rows per wave, over the steps of one split.  Keys
-// and values of a step (64 tokens) go through LDS, in two buffers: wave w
+// and values of a step (64 tokens) go through LDS, in three buffers: wave w
 // stages tokens 16w .. 16w + 15 while it computes on the step before, K as it
 // is and V already as fp16, so each value is converted once per 128 rows.
 // Bound by vector instructions: per 64 keys a wave issues about 330 of them,
@@ -499,7 +499,7 @@ typedef int v16i __attribute__((ext_vector_type(16)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr int kPromptRows = 128;
-constexpr int kRing = 2;
+constexpr int kRing = 3;
 
 template <int DC>
 __device__ __forceinline__ int k_key(int m) {
@@ -511,17 +511,26 @@ struct VPiece;
 template <>
 struct VPiece<1> {
   typedef uint16_t type;
+  static __device__ type load(__amdgpu_buffer_rsrc_t r, uint32_t lane, int row) {
+    return __builtin_amdgcn_raw_buffer_load_b16(r, lane, row, 0);
+  }
   static __device__ uint32_t word(type v, int) { return v; }
 };
 template <>
 struct VPiece<2> {
   typedef uint32_t type;
+  static __device__ type load(__amdgpu_buffer_rsrc_t r, uint32_t lane, int row) {
+    return __builtin_amdgcn_raw_buffer_load_b32(r, lane, row, 0);
+  }
   static __device__ uint32_t word(type v, int) { return v; }
 };
 template <>
 struct VPiece<4> {
-  typedef uint2 type;
-  static __device__ uint32_t word(type v, int c) { return c ? v.y : v.x; }
+  typedef uint32_t type __attribute__((ext_vector_type(2)));
+  static __device__ type load(__amdgpu_buffer_rsrc_t r, uint32_t lane, int row) {
+    return __builtin_bit_cast(type, __builtin_amdgcn_raw_buffer_load_b64(r, lane, row, 0));
+  }
+  static __device__ uint32_t word(type v, int c) { return v[c]; }
 };
 
 template <int DC, int kTeams>
@@ -553,14 +562,15 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
   const int token = valid ? row / a.group : 0;
   const int q_head = t.head * a.group + (valid ? row - token * a.group : 0);
   const int pos = t.start + token, low = a.window > 0 ? pos - a.window + 1 : 0;
-  const int first_pos = t.start + wave_row / a.group, last_pos = t.start + (min(wave_row + 32, t.rows) - 1) / a.group;
+  const int first_pos = __builtin_amdgcn_readfirstlane(t.start + wave_row / a.group);
+  const int last_pos = __builtin_amdgcn_readfirstlane(t.start + (min(wave_row + 32, t.rows) - 1) / a.group);
   v16f o[kTiles];
 #pragma unroll
   for (int i = 0; i < kTiles; ++i)
 #pragma unroll
     for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
   float m = 0.0f, l = 0.0f;
-  bool started = false;  // m means something: the row has seen a key
+  float limit = kNone;  // scores past it raise m; kNone until the row has seen a key
 
   // staging of this wave's 16 tokens of a step
   Ring& ring = rings[team];
@@ -575,24 +585,37 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
     koff[i] = (uint32_t)(tok * dim + (16 * c < dim ? 16 * c : 0));
   }
   const uint32_t voff = (uint32_t)(4 * g * dim + (2 * DC * col < dim ? 2 * DC * col : 0));
-  auto page_of = [&](int step) -> int64_t {
-    if (step >= s1) return -1;
-    const int key = t.key0(step) + 16 * wave;
-    return key < t.keys ? page_number(a.st, t.seq, key >> a.page_shift) : -1;
+  // Addresses stay in scalar registers: buffer loads take a base, a lane offset
+  // and a row's offset.  Page numbers (a step ahead) and scales are vector loads
+  // (none is a zero that the compiler does not know): the barrier below waits for
+  // scalar ones, and by their use the rows before them are waited for anyway.
+  uint32_t none;
+  asm("v_mov_b32 %0, 0" : "=v"(none));
+  auto word_at = [&](const auto* p) {
+    return *reinterpret_cast<decltype(p)>(reinterpret_cast<const char*>(p) + none);
   };
-  auto load = [&](int step, int64_t page) {
+  const int32_t* pages_of = a.st.page_table + t.seq * a.st.table_stride;
+  const uint32_t pages = (uint32_t)min(a.kv.pages, (int64_t)0x7FFFFFFF);
+  const int64_t head_bytes = (int64_t)a.kv.page_tokens * dim, page_bytes = head_bytes * a.kv.heads;
+  const int8_t *k_head = a.kv.k + t.head * head_bytes, *v_head = a.kv.v + t.head * head_bytes;
+  auto page_of = [&](int step) -> int {
+    return word_at(pages_of + (min(t.key0(min(step, s1 - 1)) + 16 * wave, t.keys - 1) >> a.page_shift));
+  };
+  auto load = [&](int step, int raw) {
+    const int number = __builtin_amdgcn_readfirstlane(raw);
     const int key = t.key0(step) + 16 * wave;
-    there = page >= 0 && page < a.kv.pages;
-    const int64_t block = there ? page * a.kv.heads + t.head : 0;
-    const int64_t at = (block * a.kv.page_tokens + (there ? key & (a.kv.page_tokens - 1) : 0)) * dim;
-    ka_raw = a.kv.k_absmax[block];
-    va_raw = a.kv.v_absmax[block];
-    const int8_t* kp = a.kv.k + at;
-    const int8_t* vp = a.kv.v + at;
+    there = key < t.keys && (uint32_t)number < pages;
+    const int64_t page = there ? number : 0;
+    const int64_t at = page * page_bytes + (key & (a.kv.page_tokens - 1)) * dim;
+    ka_raw = word_at(a.kv.k_absmax + page * a.kv.heads + t.head);
+    va_raw = word_at(a.kv.v_absmax + page * a.kv.heads + t.head);
+    constexpr int kRaw = 0x00027000;  // a plain buffer of 32-bit words
+    const auto k_rows = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(k_head + at), 0, 16 * dim, kRaw);
+    const auto v_rows = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(v_head + at), 0, 16 * dim, kRaw);
 #pragma unroll
-    for (int i = 0; i < DC; ++i) k_raw[i] = *reinterpret_cast<const v4i*>(kp + koff[i]);
+    for (int i = 0; i < DC; ++i) k_raw[i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(k_rows, koff[i], 0, 0));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v_raw[j] = *reinterpret_cast<const vpiece*>(vp + (8 * (j >> 2) + (j & 3)) * dim + voff);
+    for (int j = 0; j < 8; ++j) v_raw[j] = VPiece<DC>::load(v_rows, voff, (8 * (j >> 2) + (j & 3)) * dim);
   };
   auto store = [&](int buf) {
 #pragma unroll
@@ -620,7 +643,7 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
   // the first step's keys and values travel while the queries are split
   constexpr int kStride = kTeams;
   int step = s0 + team, buf = 0;
-  int64_t next_page = page_of(step);
+  int next_page = page_of(step);
   if (step < s1) {
     load(step, next_page);
     next_page = page_of(step + kStride);
@@ -630,40 +653,58 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
                                                   dim, g, qhi, qlo) *
                           a.scale * (1.0f / 127.0f);
 
-  // Half h (32 keys) of the step in buffer buf.  Wave priorities: staging before
-  // the products before the exponentials, so that of the two waves of a SIMD the
-  // one that others wait for, or that feeds the matrix cores, goes first (6000
-  // tokens, 20/5 heads: 290 us without, 269 with; staging alone or the other
-  // order 268 to 286).
-  auto half = [&](int step, int buf, int h) {
-    const int j0 = t.key0(step), tok = 32 * h + col;
-    const float4 sc[2] = {ring.scale[buf][2 * h], ring.scale[buf][2 * h + 1]};
-    // wave-uniform: whether all of its rows see all of the half
-    const bool all = j0 + 32 * h + 32 <= min(first_pos + 1, t.keys) &&
-                     (a.window == 0 || j0 + 32 * h > last_pos - a.window || j0 + 32 * h + 32 <= a.sinks) &&
-                     __builtin_amdgcn_readfirstlane(sc[0].w * sc[1].w != 0.0f);
-    __builtin_amdgcn_s_setprio(1);
-    v16i high, lo;
+  // Half h (32 keys) of the step in buffer buf: its softmax, with the value
+  // products of the half before and the key products of the half after it (half
+  // nh of buffer nbuf) independent of it and so among its instructions: of two
+  // waves alone on a SIMD the one hides the other's products only in part (16
+  // products and their softmax in turn 883 cycles, mixed 693).  Wave priorities:
+  // staging, which other waves wait for, before the values' products before the
+  // rest (6000 tokens, 20/5 heads: 267 us against 283 without; 512 rows of a
+  // window of 1024 54.8 against 56.9).
+  v16i high, lo;   // the next half's scores
+  v8h pf[2];       // the half before: its probabilities,
+  uint4 vf[2][kTiles];  // and its values
+  v4i kf[kTiles];
+  uint32_t kslot[kTiles];
+#pragma unroll
+  for (int c = 0; c < kTiles; ++c) kslot[c] = 16 * (col * 4 * DC + ((2 * c + g) ^ k_key<DC>(col)));
+  auto read_k = [&](int buf, int h) {  // the key of token 32 + col is that of col
+    const char* from = reinterpret_cast<const char*>(&ring.k[buf][32 * h * 4 * DC]);
+#pragma unroll
+    for (int c = 0; c < kTiles; ++c) kf[c] = *reinterpret_cast<const v4i*>(from + kslot[c]);
+  };
+  auto read_v = [&](int buf, int h) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) vf[b][i] = ring.v[buf][((2 * h + b) * kTiles + i) * 64 + lane];
+  };
+  auto key_products = [&]() {
 #pragma unroll
     for (int j = 0; j < 16; ++j) high[j] = lo[j] = 0;
 #pragma unroll
     for (int c = 0; c < kTiles; ++c) {
-      const v4i kf = ring.k[buf][tok * 4 * DC + ((2 * c + g) ^ k_key<DC>(tok))];
-      high = __builtin_amdgcn_mfma_i32_32x32x32_i8(kf, qhi[c], high, 0, 0, 0);
-      lo = __builtin_amdgcn_mfma_i32_32x32x32_i8(kf, qlo[c], lo, 0, 0, 0);
+      high = __builtin_amdgcn_mfma_i32_32x32x32_i8(kf[c], qhi[c], high, 0, 0, 0);
+      lo = __builtin_amdgcn_mfma_i32_32x32x32_i8(kf[c], qlo[c], lo, 0, 0, 0);
     }
-    // the values' operands on their way before the softmax begins (heads past
-    // 128 elements have no registers left for that)
-    uint4 vf[2][kTiles];
-    auto read_v = [&](int b) {
+  };
+  auto value_products = [&]() {
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) vf[b][i] = ring.v[buf][((2 * h + b) * kTiles + i) * 64 + lane];
-    };
-    if (DC <= 2) {
-      read_v(0);
-      read_v(1);
-    }
-    __builtin_amdgcn_sched_barrier(0);
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, vf[b][i]), pf[b], o[i], 0, 0, 0);
+  };
+  auto half = [&](int step, int buf, int h, int nbuf, int nh) {
+    const int j0 = t.key0(step);
+    const float4 sc[2] = {ring.scale[buf][2 * h], ring.scale[buf][2 * h + 1]};
+    // wave-uniform: whether all of its rows see all of the half
+    const bool all = j0 + 32 * h + 32 <= min(first_pos + 1, t.keys) &&
+                     (a.window == 0 || j0 + 32 * h > last_pos - a.window || j0 + 32 * h + 32 <= a.sinks) &&
+                     __builtin_amdgcn_readfirstlane(__float_as_int(sc[0].w) & __float_as_int(sc[1].w)) != 0;
+    read_k(nbuf, nh);
+    __builtin_amdgcn_s_setprio(1);
+    value_products();
     float x[16], top = kNone;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
@@ -671,27 +712,29 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[8 * b + j] = __builtin_fmaf((float)(high[8 * b + j] * 256 + lo[8 * b + j]), mul, add);
     }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) top = fmaxf(top, x[j]);
     if (!all) {
       asm volatile("; masked keys");  // stays a branch: most steps need none of this
       const int at = j0 + 32 * h + 4 * g, past = min(pos, t.keys - 1) - at, before = low - at, first = a.sinks - at;
+      top = kNone;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const int key = 8 * (j >> 2) + (j & 3);
         const bool seen = key <= past && (key >= before || key < first) && sc[j >> 3].w != 0.0f;
         x[j] = seen ? x[j] : -INFINITY;
+        top = fmaxf(top, x[j]);
       }
     }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) top = fmaxf(top, x[j]);
     top = halves_max(top);
-    if (__any(top > 14.0f + kSlack || (!started && top > kNone))) {
+    if (__any(top > limit)) {
       // lanes whose maximum grew (or that see their first key) take it
       asm volatile("; raised maximum");
-      const bool grows = started ? top > 14.0f : top > kNone;
+      const bool grows = top > fminf(limit, 14.0f);
       const float delta = grows ? top - 14.0f : 0.0f;
-      const float shrink = started ? __builtin_amdgcn_exp2f(-delta) : 0.0f;
+      const float shrink = limit == kNone ? 0.0f : __builtin_amdgcn_exp2f(-delta);
       m += delta;
-      started |= grows;
+      limit = grows ? 14.0f + kSlack : limit;
       l *= shrink;
 #pragma unroll
       for (int j = 0; j < 16; ++j) x[j] -= delta;
@@ -701,27 +744,25 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
         for (int j = 0; j < 16; ++j) o[i][j] *= shrink;
     }
     __builtin_amdgcn_s_setprio(0);
+    key_products();
+    read_v(buf, h);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      if (DC > 2) read_v(b);
-      v8h pf;
       float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float p = __builtin_amdgcn_exp2f(x[8 * b + j]);
         sum += p;
-        pf[j] = (_Float16)p;
+        pf[b][j] = (_Float16)p;
       }
       l = __builtin_fmaf(sum, sc[b].z, l);
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i)
-        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, vf[b][i]), pf, o[i], 0, 0, 0);
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
 
-  // A team's step is staged while the one before is worked on, behind one
-  // barrier per step: a wave that stores the n-th has passed the barrier after
-  // the (n - 2)-th, whose buffer it takes.
+  // A team's step n + 1 is staged while step n is worked on, behind one barrier
+  // between the halves of n: the buffer it takes was last read (values of the
+  // second half of n - 2) before the barrier of n - 1.
   const int rounds = (s1 - s0 + kStride - 1) / kStride;
   if (step < s1) store(0);
   if (step + kStride < s1) {
@@ -729,18 +770,32 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
     next_page = page_of(step + 2 * kStride);
   }
   __syncthreads();
-  for (int round = 0; round < rounds; ++round, step += kStride, buf ^= 1) {
+  if (busy && step < s1) {
+    read_k(0, 0);
+    key_products();
+    read_v(0, 0);  // anything finite: the first half has none before it
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) pf[b][j] = (_Float16)0.0f;
+  }
+  for (int round = 0; round < rounds; ++round, step += kStride) {
     const bool mine = busy && step < s1;
-    if (mine) half(step, buf, 0);
+    const int next = buf == kRing - 1 ? 0 : buf + 1;
+    if (mine) half(step, buf, 0, buf, 1);
     __builtin_amdgcn_s_setprio(3);
-    if (step + kStride < s1) store(buf ^ 1);
+    if (step + kStride < s1) store(next);
     if (step + 2 * kStride < s1) {
       load(step + 2 * kStride, next_page);
       next_page = page_of(step + 3 * kStride);
     }
-    if (mine) half(step, buf, 1);
     __syncthreads();
+    if (mine) half(step, buf, 1, next, 0);
+    buf = next;
   }
+  if (busy && s0 + team < s1) value_products();
+  if (kTeams == 2) __syncthreads();  // before the teams meet in the buffers
+  bool started = limit != kNone;
 
   l += __shfl_xor(l, 32, 64);
   if (kTeams == 2) {
