@@ -481,11 +481,11 @@ __global__ __launch_bounds__(kThreads, DC == 1 ? 4 : DC == 2 ? (kPages == 1 ? 3 
 // and values of a step (64 tokens) go through LDS, in three buffers: wave w
 // stages tokens 16w .. 16w + 15 while it computes on the step before, K as it
 // is and V already as fp16, so each value is converted once per 128 rows.
-// Bound by vector instructions: per 64 keys a wave issues about 330 of them,
-// 32 of which (the exponentials) take four turns, against 32 MFMAs of 32 cycles;
-// with two waves per SIMD the vector pipe is busy for two thirds of the time.
-// 24000 tokens of 20/5 heads of 128: 850 TFLOP/s (a bf16 library product of 8192
-// cubed reaches 1217); 6000 tokens: 252 us, 730 TFLOP/s, where the longest tiles
+// Bound by instruction issue: per 32 keys a wave issues about 145 vector
+// instructions, 16 of which (the exponentials) take two turns, against 16 MFMAs
+// of 32 cycles, and each MFMA takes two to three turns of issue itself.
+// 24000 tokens of 20/5 heads of 128: 920 TFLOP/s (a bf16 library product of 8192
+// cubed reaches 1217); 6000 tokens: 220 us, 837 TFLOP/s, where the longest tiles
 // (94 steps) set the end.
 // One team of four waves takes all steps, two workgroups to a CU; or two teams
 // take them in turn, each with its own running state and buffers, one workgroup
@@ -947,20 +947,22 @@ struct Plan {
 // Workgroups of 16 rows (k_attn) or of 128 (k_attn_prompt).  The former read
 // and convert the keys and values once per 16 rows, but their four waves share
 // a tile's steps, so that few rows, and many over few keys, are done sooner:
-// 21 x 1200 rows of 64 over up to 600 keys 13 us against 18, 16 x 756 12.8
-// against 22, 5 x 4000 of 128 over 1000 34 against 34; but 28 x 2644 of 128 over
-// 721 keys 60 us against 36, and 64 tokens of 20 heads over 4064 keys 31 against 26.
+// 25 x 1200 rows of 64 over up to 600 keys 14 us against 16, 5 x 2800 of 128 over
+// 700 19 against 23, 15 x 400 over 900 15 against 24; but 40 x 1200 of 64 18
+// against 16, 40 x 512 of 128 over 640 26 against 21, 28 x 2644 over 721 50 against
+// 32, and 64 tokens of 20 heads over 4064 keys 31 against 25.  Between 16000 and
+// 30000 tile steps either may win, by 15 %.
 bool few_rows(int64_t rows, int64_t lists, int64_t steps, int dim) {
   const int64_t tiles = lists * ((rows + 15) / 16), chunks = (dim + 63) / 64;
-  return rows < 64 || (steps <= 32 && tiles * steps * chunks < 40000);
+  return rows < 64 || (steps <= 32 && tiles * steps * chunks < 25000);
 }
 
 // Two teams (one workgroup of eight waves to a CU) while the tiles fill the
 // 256 CUs less than twice and have many steps: a tile then takes half the
-// time (376 tiles of up to 94 steps: 133 us against 185 with one team, 256 of
-// 47: 68 against 79, 40 of 16: 34 against 42).  One team (two independent
-// workgroups to a CU) where there are tiles enough (940 of up to 94: 290 us
-// against 302) or, past one per CU, few steps (480 of 20: 65 against 73).
+// time (470 tiles of up to 47 steps: 82 us against 99 with one team, 256 of 47: 58
+// against 76, 235 of 24: 39 against 51).  One team (two independent workgroups to
+// a CU) where there are tiles enough (940 of up to 94: 245 us against 263) or,
+// past one per CU, few steps (480 of 20: 55 against 64).
 bool two_teams(int dim, int64_t tiles, int64_t steps) {
   return dim <= 128 && ((tiles < 256 && steps > 6) || (tiles < 512 && steps > 24));
 }
