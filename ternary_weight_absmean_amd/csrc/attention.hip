@@ -987,9 +987,16 @@ Plan make_plan(const KvView& kv, int64_t seqs, int64_t max_new, int64_t max_len,
     const int64_t wanted = p.tiles < blocks ? blocks / p.tiles : 1, most = (steps + least - 1) / least;
     return wanted < most ? wanted : most;
   };
+  // Up to this many steps a split gives less than the join and its launch take
+  // (steps of 128 elements, one workgroup against splits: 12 steps 9.5 us against
+  // 10.6, 16 10.5 against 10.6, 24 13.1 against 10.9; 320 tiles of 16 18.7 against
+  // 21.4).  Longer heads' steps take longer, which a few tiles' own time shows
+  // (256 elements, 5 tiles of 16 steps 16.7 against 13.0, 80 of 11 16.8 against
+  // 14.9; but 320 of 10 26 against 36).
+  const int64_t unsplit = p.tile_rows == 16 && kv.dim > 128 && p.tiles < 160 ? kUnsplit / 2 : kUnsplit;
   int64_t splits = 1;
-  if (steps <= kUnsplit) {
-    // the join and its launch would take longer
+  if (steps <= unsplit) {
+    // one workgroup
   } else if (p.tile_rows == 16) {
     const int64_t full = pick(kTargetBlocks, 4 * kWaves), few = pick(1024, kWaves);
     splits = full > few ? full : few;
