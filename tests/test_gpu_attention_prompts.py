@@ -9,9 +9,11 @@ import numpy as np
 import pytest
 import torch
 
-from _gpu import say
+import _block
+import ternary_weight_absmean_amd as bl
+from _gpu import DEV, bf16, bf16_bits_to_f64, host, say
 from test_gpu_attention import check
-from test_gpu_kv_cache import Case, heads
+from test_gpu_kv_cache import Case, heads, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +112,43 @@ def test_workspace_covers_every_window():
     rng = np.random.default_rng(15)
     for ctx, new, q_heads, window in [(4480, 33, 2, 4352), (6000, 64, 1, 2176), (4000, 1, 4, 1100), (9000, 20, 4, 4000)]:
         run(rng, [ctx], [new], 1, q_heads, 16, 64, window=window)
+
+
+@pytest.mark.parametrize("tokens", [512, 513, 1024, 1025])
+@pytest.mark.parametrize("dim,seqs", [(256, 1), (192, 2), (128, 1), (64, 3)])
+def test_either_side_of_a_split_along_the_keys(tokens, dim, seqs):
+    """8 and 9 (long heads), 16 and 17 steps: one workgroup and several; the other sequences are short."""
+    run(np.random.default_rng(tokens + dim), [tokens - 1] + [30] * (seqs - 1), [1] * seqs, 2, 8, dim, 64)
+
+
+@pytest.mark.parametrize("new", [97, 100, 103])
+def test_either_side_of_the_kernel_for_many_rows(new):
+    """12 heads of 128 over 10 and 11 steps: 23040 to 27456 tile steps of 16 rows."""
+    run(np.random.default_rng(new), [540, 540, 440, 540], [new, new, 3, new], 12, 48, 128, 32)
+
+
+def test_prompts_past_32_bits():
+    """The same sequence in the first pages of a cache and past its 2^32-th byte gives the same bits."""
+    rng = np.random.default_rng(16)
+    n_heads, page, dim, ctx, new = 8, 64, 128, 2050, 64
+    need = -(-(ctx + new) // page)
+    pages = (1 << 32) // (n_heads * page * dim) + 2 * need
+    c = Case(rng, [ctx], [new], n_heads, dim, page, spare=0)
+    c.table = np.arange(need)[None]
+    say("bl_attention prompts past 2^32 bytes")
+    big = [torch.empty((pages, n_heads, page, dim), dtype=torch.int8, device=DEV) for _ in range(2)]
+    top = [torch.ones((pages, n_heads), device=DEV) for _ in range(2)]
+    table = np.stack([np.arange(need), pages - 1 - np.arange(need)])
+    for t, a, codes, absmax in zip(big, top, (c.k, c.v), (c.ka, c.va)):
+        for row in table:
+            t[torch.from_numpy(row).to(DEV)] = torch.from_numpy(codes).to(DEV)
+            a[torch.from_numpy(row).to(DEV)] = torch.from_numpy(absmax).to(DEV)
+    batch = bl.KVBatch(i32(table), i32([ctx, ctx]), i32([0, new, 2 * new]), 2 * new, new, ctx + new)
+    q = heads(rng, new, 32, dim)
+    one = bf16(_block.bits(q))
+    out = bl.bl_attention(bl.KVCache(*big, *top), batch, torch.cat([one, one]))
+    torch.cuda.synchronize()
+    assert torch.equal(out[:new], out[new:])
+    want, _, bound, _ = _block.attention(q, c.k, c.ka, c.v, c.va, c.table, c.start, c.offsets,
+                                         np.float64(np.float32(dim ** -0.5)))
+    assert (np.abs(bf16_bits_to_f64(host(out[:new])) - want) <= bound + _block.U16 * (np.abs(want) + bound)).all()
