@@ -220,3 +220,11 @@ def test_cache_longer_than_32_bits():
     want, _, bound, _ = _block.attention(bf16_bits_to_f64(host(one[:1])), c.k, c.ka, c.v, c.va, c.table, c.start, c.offsets,
                                          np.float64(np.float32(dim ** -0.5)))
     assert (np.abs(bf16_bits_to_f64(host(out[:1])) - want) <= bound + _block.U16 * (np.abs(want) + bound)).all()
+
+
+def test_workspace_on_the_host_is_refused():
+    c = Case(np.random.default_rng(61), [40], [1], 2, 64, 16)
+    cache, batch = c.device()
+    q = bf16(_block.bits(heads(c.rng, 1, 4, 64)))
+    with pytest.raises(ValueError, match="workspace"):
+        bl.bl_attention(cache, batch, q, workspace=torch.empty(1 << 16, dtype=torch.uint8))

@@ -14,7 +14,7 @@ import torch
 
 import _block
 import ternary_weight_absmean_amd as bl
-from _gpu import bf16, bf16_bits_to_f64, f32, host, say
+from _gpu import DEV, bf16, bf16_bits_to_f64, f32, host, say
 
 pytestmark = pytest.mark.gpu
 
@@ -186,3 +186,11 @@ def test_norm_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
         assert torch.equal(grads[0], eager[0]) and torch.equal(grads[1], eager[1])
+
+
+def test_backward_workspace_on_the_host_is_refused():
+    dn, r, w = torch.ones((2, 64), device=DEV), torch.ones((2, 64), dtype=torch.bfloat16, device=DEV), torch.ones(64, device=DEV)
+    with pytest.raises(ValueError, match="workspace"):
+        bl.bl_rmsnorm_backward(dn, r, w, workspace=torch.empty(1 << 16, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="workspace"):
+        bl.bl_rmsnorm_backward(dn, r, w, workspace=torch.empty((1 << 16, 2), dtype=torch.uint8, device=DEV)[:, 0])
