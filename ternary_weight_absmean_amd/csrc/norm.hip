@@ -170,9 +170,9 @@ __global__ __launch_bounds__(T) void k_rmsnorm_quant(const uint4* x, const uint4
 // sums in registers; per row one reduction (sum r^2 and sum dn w r).  The
 // workgroups' sums go to the workspace and a second kernel adds them in a
 // fixed order, so no atomics and the same bits every time.  HBM-bound: 4096 x
-// 8192 with dr (336 MB, and 17 MB of partial sums written and read again) 68 +
-// 5 us; 333 x 6912 8.8 + 4.1 us, one row per workgroup, so two round trips and a
-// reduction each.
+// 8192 with dr (336 MB, and 8 MB of partial sums written and read again) 65 us,
+// 5.2 TB/s; 333 x 6912 11.1 us, one or two rows per workgroup, so two round trips
+// and a reduction in each kernel.
 template <int T, int kC>
 __global__ __launch_bounds__(T) void k_rmsnorm_backward(const uint4* __restrict__ dn, const uint4* __restrict__ r,
                                                         const uint4* __restrict__ w, const uint4* dr, int64_t m, int k8,
@@ -185,6 +185,21 @@ __global__ __launch_bounds__(T) void k_rmsnorm_backward(const uint4* __restrict_
   for (int c = 0; c < kC; ++c)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[c][j] = 0.0f;
+  // the weights stay in registers (8192 x 640 16 us against 19 with two reads of
+  // them per row, 4096 x 2560 24 against 27, 4096 x 8192 70 against 72); the longest
+  // rows leave none for that (scratch: 1000 x 32768 144 against 91)
+  constexpr bool kHold = kC < 8;
+  uint4 vw[kHold ? 2 * kC : 1];
+  if (kHold) {
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+      vw[2 * c] = buffer_load16(wr, (uint32_t)(tid + c * T) * 32);
+      vw[2 * c + 1] = buffer_load16(wr, (uint32_t)(tid + c * T) * 32 + 16);
+    }
+  }
+  auto weight = [&](int c, int i) {
+    return kHold ? vw[kHold ? 2 * c + i : 0] : buffer_load16(wr, (uint32_t)(tid + c * T) * 32 + 16 * i);
+  };
   int turn = 0;
   for (int64_t row = blockIdx.x; row < m; row += gridDim.x, turn ^= 1) {
     const __amdgpu_buffer_rsrc_t nr = buffer_rsrc(dn + row * k8 * 2, (uint32_t)(k8 * 32));
@@ -204,8 +219,7 @@ __global__ __launch_bounds__(T) void k_rmsnorm_backward(const uint4* __restrict_
     for (int c = 0; c < kC; ++c) {
       float rv[8];
       unpack_bf16x8(vr[c], rv);
-      const uint4 w0 = buffer_load16(wr, (uint32_t)(tid + c * T) * 32);
-      const uint4 w1 = buffer_load16(wr, (uint32_t)(tid + c * T) * 32 + 16);
+      const uint4 w0 = weight(c, 0), w1 = weight(c, 1);
       const uint32_t wb[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
       const uint32_t nb[8] = {vn[2 * c].x,     vn[2 * c].y,     vn[2 * c].z,     vn[2 * c].w,
                               vn[2 * c + 1].x, vn[2 * c + 1].y, vn[2 * c + 1].z, vn[2 * c + 1].w};
@@ -240,7 +254,7 @@ __global__ __launch_bounds__(T) void k_rmsnorm_backward(const uint4* __restrict_
       unpack_bf16x8(vr[i], rv);
       if (kC == 8) vg[i] = buffer_load16(gr, (uint32_t)at * 16);
       unpack_bf16x8(vg[i], g);
-      const uint4 w0 = buffer_load16(wr, (uint32_t)at * 32), w1 = buffer_load16(wr, (uint32_t)at * 32 + 16);
+      const uint4 w0 = weight(i, 0), w1 = weight(i, 1);
       const uint32_t wb[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
       const uint32_t nb[8] = {vn[2 * i].x,     vn[2 * i].y,     vn[2 * i].z,     vn[2 * i].w,
                               vn[2 * i + 1].x, vn[2 * i + 1].y, vn[2 * i + 1].z, vn[2 * i + 1].w};
@@ -287,11 +301,12 @@ __global__ __launch_bounds__(kDwCols / 4 * kDwSlots) void k_rmsnorm_dw(const flo
 }
 
 // Workgroups of the backward kernel: about as many as run at once, since each
-// writes a row of partial sums.  4096 x 8192: 74 us with 512, 78 with 256 and
-// 79 with 1024; 8192 x 640: 18 us with 1024, 23 with 512; 1000 x 28672: 81 us
-// with 256, 93 with 512.
+// writes a row of partial sums.  4096 x 8192: 65 us with 256, 70 with 512; 4096 x
+// 2560: 24 with 512, 30 with 256, 27 with 1024; 8192 x 2048: 35 with 512, 39 with
+// 1024; 8192 x 1024: 19.5 with 1024, 22.5 with 512; 8192 x 640: 16 with 1024, 21
+// with 512; 1000 x 28672: 81 us with 256, 93 with 512.
 int back_blocks(int64_t m, int64_t k) {
-  const int64_t most = k <= 2048 ? 1024 : k <= 8192 ? 512 : 256;
+  const int64_t most = k <= 1024 ? 1024 : k <= 4096 ? 512 : 256;
   return (int)(m < most ? m : most);
 }
 
@@ -342,6 +357,8 @@ hipError_t launch_rmsnorm_backward(const float* dn, const uint16_t* r, const flo
     go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
   else if (k8 <= 1024)
     go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  else if (k8 <= 2048)  // 2000 x 16384 72 us against 91 with eight chunks per thread, 1500 x 12288 42 against 58
+    go(integral_constant<int, 512>{}, integral_constant<int, 4>{});
   else
     go(integral_constant<int, 512>{}, integral_constant<int, 8>{});
   hipError_t e = hipGetLastError();

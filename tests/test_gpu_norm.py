@@ -194,3 +194,10 @@ def test_backward_workspace_on_the_host_is_refused():
         bl.bl_rmsnorm_backward(dn, r, w, workspace=torch.empty(1 << 16, dtype=torch.uint8))
     with pytest.raises(ValueError, match="workspace"):
         bl.bl_rmsnorm_backward(dn, r, w, workspace=torch.empty((1 << 16, 2), dtype=torch.uint8, device=DEV)[:, 0])
+
+
+@pytest.mark.parametrize("m,k", [(259, 6912), (300, 4160), (515, 2048), (1030, 1024), (257, 16384), (258, 12352),
+                                 (257, 8256), (259, 16448)])
+def test_backward_of_more_rows_than_workgroups(m, k):
+    """A workgroup's second row, in each of the kernel's forms."""
+    test_backward_matches_reference(m, k, True)
