@@ -420,7 +420,12 @@ typedef struct bl_kv_cache {
  * max_new and max_len bound offsets[s + 1] - offsets[s] and start[s] +
  * offsets[s + 1] - offsets[s]; max_len <= table_stride * page_tokens.  A page
  * number outside 0 .. pages - 1 marks a page that is not there: nothing is
- * written to it, reading it gives zeros, attention skips it. */
+ * written to it, reading it gives zeros, attention skips it.
+ * The host cannot see start and offsets.  Values of them that break these
+ * bounds give no error and no access outside a buffer: start is taken as at
+ * least 0, a sequence's tokens as at most max_new inside 0 .. tokens - 1,
+ * positions past the table as pages that are not there, and attention sees no
+ * position from max_len on. */
 typedef struct bl_kv_batch {
     const int32_t* page_table; /* device [seqs][table_stride] */
     const int32_t* start;      /* device [seqs], >= 0         */

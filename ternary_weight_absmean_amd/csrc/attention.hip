@@ -47,6 +47,7 @@ struct Attn {
   const uint16_t* q;
   int64_t qt, qh;
   int q_heads, group, page_shift;
+  int max_len;
   int window, sinks;
   float scale;       // of q . k, in base 2
   int tile_rows;     // rows of a tile (16 or kPromptRows)
@@ -70,13 +71,33 @@ __device__ __forceinline__ int64_t page_number(const KvStep& st, int seq, int64_
   return uniform_load(st.page_table + seq * st.table_stride + index);
 }
 
+// The steps of keys that rows at positions first_pos .. last_pos take.  The
+// lengths that the host planned for end at max_len, wherever the device's
+// positions lead: keys from there on are not seen, so that no tile has more
+// steps than the plan and its workspace hold.  There is one step at least (all
+// masked, if nothing is visible), so every row is written.
+struct Span {
+  int keys;  // keys 0 .. keys-1 may be visible
+  int sink_steps, base, steps;
+  __host__ __device__ int key0(int step) const { return (step < sink_steps ? step : base + step - sink_steps) * kStep; }
+};
+
+__host__ __device__ inline Span span_of(int first_pos, int last_pos, int max_len, int window, int sinks) {
+  Span s;
+  s.keys = last_pos < max_len ? last_pos + 1 : max_len;
+  const int last = (s.keys + kStep - 1) / kStep, from = first_pos - window + 1;
+  s.base = window > 0 && from > 0 ? from / kStep : 0;
+  if (s.base > last - 1) s.base = last - 1;
+  s.sink_steps = (sinks + kStep - 1) / kStep;
+  if (s.sink_steps > s.base) s.sink_steps = s.base;
+  s.steps = s.sink_steps + last - s.base;
+  return s;
+}
+
 // The rows and steps of one tile.
-struct Tile {
+struct Tile : Span {
   int seq, head, begin, rows, row0, start;
   int first_pos, last_pos;  // positions of its first and last row
-  int keys;                 // keys 0 .. keys-1 may be visible
-  int sink_steps, base, steps;
-  __device__ int key0(int step) const { return (step < sink_steps ? step : base + step - sink_steps) * kStep; }
 };
 
 // Workgroups are dealt to the eight XCDs in turn: eight tiles are taken
@@ -110,12 +131,7 @@ __device__ __forceinline__ bool find_tile(const Attn& a, int index, Tile& t) {
   t.start = st.start_from(start);
   t.first_pos = t.start + t.row0 / a.group;
   t.last_pos = t.start + (min(t.row0 + a.tile_rows, t.rows) - 1) / a.group;
-  const int64_t room = a.st.table_stride << a.page_shift;
-  t.keys = (int)min((int64_t)t.last_pos + 1, room);
-  const int last = (t.keys + kStep - 1) / kStep;
-  t.base = a.window > 0 ? min(max(0, t.first_pos - a.window + 1) / kStep, last) : 0;
-  t.sink_steps = min((a.sinks + kStep - 1) / kStep, t.base);
-  t.steps = t.sink_steps + last - t.base;
+  static_cast<Span&>(t) = span_of(t.first_pos, t.last_pos, a.max_len, a.window, a.sinks);
   return true;
 }
 
@@ -1045,6 +1061,7 @@ hipError_t launch_attention(const KvView& kv, const KvStep& st, int64_t seqs, in
   a.q_heads = q_heads;
   a.group = q_heads / kv.heads;
   a.page_shift = __builtin_ctz((unsigned)kv.page_tokens);
+  a.max_len = (int)max_len;
   a.window = (int)window;
   a.sinks = (int)sinks;
   a.scale = scale * kLog2e;

@@ -112,14 +112,15 @@ struct KvView {
 };
 
 // The tokens of a step.  What the host cannot see (device integers) is brought
-// into range here, so that no value of them leads outside a buffer.
+// into range here and, for the lengths that the attention's plan rests on, in
+// its span_of, so that no value of them leads outside a buffer.
 struct KvStep {
   const int32_t *page_table, *start, *offsets;
   int64_t table_stride;
   int tokens, max_new;
-  __device__ int begin_of(int from) const { return min(max(from, 0), tokens); }
-  __device__ int count_of(int begin, int to) const { return min(min(max(to, begin), tokens) - begin, max_new); }
-  __device__ static int start_from(int start) { return min(max(start, 0), 1 << 29); }
+  __host__ __device__ int begin_of(int from) const { return min(max(from, 0), tokens); }
+  __host__ __device__ int count_of(int begin, int to) const { return min(min(max(to, begin), tokens) - begin, max_new); }
+  __host__ __device__ static int start_from(int start) { return min(max(start, 0), 1 << 29); }
   __device__ int begin(int s) const { return begin_of(offsets[s]); }
   __device__ int count(int s, int begin) const { return count_of(begin, offsets[s + 1]); }
   __device__ int start_of(int s) const { return start_from(start[s]); }
