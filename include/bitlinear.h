@@ -480,8 +480,9 @@ size_t bl_attention_workspace_bytes(const bl_kv_cache* cache, const bl_kv_batch*
  * Keys are read as stored; a query row enters the products as 16-bit integers
  * relative to its absmax; softmax statistics and sums are fp32; the weights
  * enter the product with v in fp16, scaled so that none above 2^-28 of the
- * row's largest contribution loses precision.  The result does not depend on
- * the order in which workgroups run.
+ * row's largest contribution (weight times absmax of its page) loses precision.
+ * An absmax of v below 2^-64, such as a page of zeros has, counts as 2^-64.
+ * The result does not depend on the order in which workgroups run.
  * Errors: BL_ERR_NULL, BL_ERR_SHAPE (also q_heads no multiple of heads, sinks
  * without a window, scale not finite), BL_ERR_ALIGN, BL_ERR_WORKSPACE, BL_ERR_HIP. */
 bl_status bl_attention(const bl_kv_cache* cache, const bl_kv_batch* batch, const uint16_t* q, int64_t q_token_stride,

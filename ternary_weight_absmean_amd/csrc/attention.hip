@@ -8,7 +8,10 @@
 // m being the running maximum of t.  Taking va into the exponent keeps every P
 // at or below 2^14 whatever the pages' scales, so P fits fp16 with 11 bits of
 // precision for every term above 2^-28 of the row's largest contribution; l is
-// summed in fp32 from the unrounded P.
+// summed in fp32 from the unrounded P.  A page of zeros has an absmax of 0: it
+// counts as 2^-64, below which bl_kv_append keeps none, so that its weights
+// reach l (at most 2^29 keys of 2^15.5 * 2^64) and do not push the others'
+// below fp16's range.
 //
 // Products.  Keys stay int8: a query row becomes 16-bit integers (absmax /
 // 32512 per step), split into signed high and low bytes, and two int8 MFMAs
@@ -38,6 +41,7 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kStep = 64;       // keys per step of a wave
+constexpr float kLeastAbsmax = 0x1p-64f;
 constexpr float kNone = -1e30f;  // a running maximum that nothing has raised
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -345,7 +349,7 @@ __global__ __launch_bounds__(kThreads, DC == 1 ? 4 : DC == 2 ? (kPages == 1 ? 3 
 #pragma unroll
     for (int i = 0; i < kPages; ++i) {
       all = all && now.there[i];
-      va[i] = now.there[i] && now.va[i] > 0.0f ? now.va[i] : 1.0f;
+      va[i] = fmaxf(now.va[i], kLeastAbsmax);
     }
     v4i high[4], lo[4];
 #pragma unroll
@@ -651,7 +655,7 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
                      halves_of(w[4][i >> 2], w[5][i >> 2], i & 3), halves_of(w[6][i >> 2], w[7][i >> 2], i & 3));
     }
     if (lane == 0) {
-      const float va = there && va_raw > 0.0f ? va_raw : 1.0f;
+      const float va = fmaxf(va_raw, kLeastAbsmax);
       ring.scale[buf][wave] = make_float4(ka_raw, __builtin_amdgcn_logf(va), __builtin_amdgcn_rcpf(va), there ? 1.0f : 0.0f);
     }
   };
