@@ -322,12 +322,13 @@ bl_status bl_unpack_ternary(const uint8_t* packed, int64_t n, int64_t k, int8_t*
  * The norm and its codes are those of the fp32 sum, not of the rounded r;
  * alpha is the fp32 maximum (bl_quant_act's is a bf16 value, as its input is).
  *   x, residual  [m][k] bf16; residual may be NULL.
- *   weight       [k] fp32.   eps finite, >= 0.
+ *   weight       [k] fp32.   eps finite, >= 0.  Where mean h^2 + eps is 0 (a row
+ *                of zeros without an eps) c is 0, here and in the gradients.
  *   r, y, xhat   out [m][k] bf16, each NULL to skip it; r may be x or residual.
  *   xq, alpha    out [m][k] int8 and [m] fp32, both or neither NULL.
  * At least one output is required.  k is a multiple of 64, at most
  * BL_MAX_NORM_K (a row stays in registers); |h| below 2^56, so that the sum of
- * squares is finite.  x, residual, weight and the [m][k] outputs are 16-byte
+ * squares is finite, and, where eps is 0, mean h^2 no fp32 denormal.  x, residual, weight and the [m][k] outputs are 16-byte
  * aligned.
  * Errors: BL_ERR_NULL, BL_ERR_SHAPE (also a bad eps), BL_ERR_ALIGN, BL_ERR_HIP. */
 #define BL_MAX_NORM_K 32768

@@ -29,6 +29,10 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&f)[8]) {
                     f32x2_to_bf16x2(f[6], f[7]));
 }
 
+// 1 / sqrt(v), correctly rounded division and root; 0 for v = 0, which a row of
+// zeros has without an eps: its norm is zeros and it adds nothing to a gradient.
+__device__ __forceinline__ float rsqrt_or_zero(float v) { return v == 0.0f ? 0.0f : 1.0f / sqrtf(v); }
+
 // A store that leaves the caches to others: the sum and the bf16 outputs are
 // not what the next kernel reads (that is xq), and by the time of their own next
 // use other kernels have passed.  2048 x 8192 with residual: 23 us against 31
@@ -129,7 +133,7 @@ __global__ __launch_bounds__(T) void k_rmsnorm_quant(const uint4* x, const uint4
       top = fmaxf(top, wave_part[1][i]);
     }
   }
-  const float c = 1.0f / sqrtf(sum / (float)(k8 * 8) + eps);  // correctly rounded division and root
+  const float c = rsqrt_or_zero(sum / (float)(k8 * 8) + eps);
   const float a = top * c;
   const float s = 127.0f / fmaxf(a, 1e-5f);
   const float step = a / 127.0f;
@@ -244,7 +248,7 @@ __global__ __launch_bounds__(T) void k_rmsnorm_backward(const uint4* __restrict_
       inner += wave_part[turn][1][i];
     }
     const float inv = 1.0f / (float)(k8 * 8);
-    const float c = 1.0f / sqrtf(square * inv + eps);
+    const float c = rsqrt_or_zero(square * inv + eps);
     const float back = inner * inv * c * c;
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
