@@ -473,7 +473,8 @@ size_t bl_attention_workspace_bytes(const bl_kv_cache* cache, const bl_kv_batch*
  * over the positions j <= p of its sequence, p being the query's own; with
  * window > 0 only those with p - j < window or j < sinks.  Query head h reads
  * cache head h / (q_heads / heads).  A query that sees nothing (its pages are
- * not there) gives zeros.
+ * not there) gives zeros; one that holds a NaN or an infinity, or sees a page
+ * with such an absmax, gives NaN.
  *   q      bf16 [tokens][q_heads][dim], strides in elements (multiples of 8).
  *   out    bf16 [tokens][q_heads][dim], contiguous.
  *   lse    NULL, or out fp32 [tokens][q_heads]: log sum_j exp(scale * q . k_j)

@@ -172,9 +172,11 @@ __device__ __forceinline__ float split_query(const uint16_t* row, bool valid, in
   }
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) most = absmax_step(absmax_step(most, d[c][0]), d[c][1]);
-  float top = __uint_as_float((uint32_t)max(most.x, most.y) << 16);
-  if (kWidth == 64) top = fmaxf(top, __shfl_xor(top, 16, 64));
-  top = fmaxf(top, __shfl_xor(top, 32, 64));
+  // as bits, which order like the values and hold a NaN (then every score is one)
+  int top_bits = (int)max(most.x, most.y) << 16;
+  if (kWidth == 64) top_bits = max(top_bits, __shfl_xor(top_bits, 16, 64));
+  top_bits = max(top_bits, __shfl_xor(top_bits, 32, 64));
+  const float top = __int_as_float(top_bits);
   const float s = top > 0x1p-100f ? 32512.0f / top : 0.0f;
   // x * s + 1.5 * 2^23 has the code (at most 32512 in magnitude) in its low
   // bytes; 128 more carries the low byte's sign into the high one
@@ -349,7 +351,7 @@ __global__ __launch_bounds__(kThreads, DC == 1 ? 4 : DC == 2 ? (kPages == 1 ? 3 
 #pragma unroll
     for (int i = 0; i < kPages; ++i) {
       all = all && now.there[i];
-      va[i] = fmaxf(now.va[i], kLeastAbsmax);
+      va[i] = now.va[i] < kLeastAbsmax ? kLeastAbsmax : now.va[i];
     }
     v4i high[4], lo[4];
 #pragma unroll
@@ -415,7 +417,8 @@ __global__ __launch_bounds__(kThreads, DC == 1 ? 4 : DC == 2 ? (kPages == 1 ? 3 
         x[i][j] = __builtin_amdgcn_exp2f(x[i][j]);
         sum += x[i][j];
       }
-      l = __builtin_fmaf(sum, __builtin_amdgcn_rcpf(va[i * kPages / 4]), l);
+      // a NaN among the absmax is in the scores of the keys that see it, and only theirs
+      l = __builtin_fmaf(sum, __builtin_amdgcn_rcpf(fmaxf(va[i * kPages / 4], kLeastAbsmax)), l);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -477,13 +480,13 @@ __global__ __launch_bounds__(kThreads, DC == 1 ? 4 : DC == 2 ? (kPages == 1 ? 3 
     for (int w = 0; w < kWaves; ++w) x[i] = __builtin_fmaf(weight[w], lds_o[w][r][seg + i], x[i]);
   }
   if (whole) {
-    const float mul = sum > 0.0f ? (512.0f / 127.0f) / sum : 0.0f;
+    const float mul = sum != 0.0f ? (512.0f / 127.0f) / sum : 0.0f;
     if (seg < dim) {
       uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + out_row * dim + seg);
 #pragma unroll
       for (int i = 0; i < 2 * DC; ++i) dst[i] = f32x2_to_bf16x2(x[2 * i] * mul, x[2 * i + 1] * mul);
     }
-    if (a.lse && (tid & 15) == 0) a.lse[out_row] = sum > 0.0f ? (__log2f(sum) + top - 14.0f) * kLn2 : -INFINITY;
+    if (a.lse && (tid & 15) == 0) a.lse[out_row] = sum != 0.0f ? (__log2f(sum) + top - 14.0f) * kLn2 : -INFINITY;
     return;
   }
   const int64_t slot = out_row * a.splits + split;
@@ -655,8 +658,10 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
                      halves_of(w[4][i >> 2], w[5][i >> 2], i & 3), halves_of(w[6][i >> 2], w[7][i >> 2], i & 3));
     }
     if (lane == 0) {
+      // a NaN among the absmax is in the scores of the keys that see it, and only theirs
       const float va = fmaxf(va_raw, kLeastAbsmax);
-      ring.scale[buf][wave] = make_float4(ka_raw, __builtin_amdgcn_logf(va), __builtin_amdgcn_rcpf(va), there ? 1.0f : 0.0f);
+      ring.scale[buf][wave] = make_float4(ka_raw, __builtin_fmaf(va_raw, 0.0f, __builtin_amdgcn_logf(va)),
+                                          __builtin_amdgcn_rcpf(va), there ? 1.0f : 0.0f);
     }
   };
 
@@ -857,7 +862,7 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
   }
   if (!valid) return;
   const int64_t out_row = (int64_t)(t.begin + token) * a.q_heads + q_head;
-  const float mul = l > 0.0f ? (512.0f / 127.0f) / l : 0.0f;
+  const float mul = l != 0.0f ? (512.0f / 127.0f) / l : 0.0f;
   const int64_t slot = out_row * a.splits + split;
   // o[i][4b + j] is element 2 DC (8b + 4g + j) + i: 8 DC adjacent ones per b
 #pragma unroll
@@ -888,7 +893,7 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
     if (!whole)
       *reinterpret_cast<float2*>(a.part_ml + slot * 2) = make_float2(started ? m : kNone, l);
     else if (a.lse)
-      a.lse[out_row] = l > 0.0f ? (__log2f(l) + m - 14.0f) * kLn2 : -INFINITY;
+      a.lse[out_row] = l != 0.0f ? (__log2f(l) + m - 14.0f) * kLn2 : -INFINITY;
   }
 }
 
@@ -945,11 +950,11 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(Attn a) {
     }
   }
   if (!valid) return;
-  const float mul = sum > 0.0f ? (512.0f / 127.0f) / sum : 0.0f;
+  const float mul = sum != 0.0f ? (512.0f / 127.0f) / sum : 0.0f;
   if (lane < kLanes && at < dim)
     *reinterpret_cast<uint2*>(a.out + out_row * dim + at) =
         make_uint2(f32x2_to_bf16x2(x[0] * mul, x[1] * mul), f32x2_to_bf16x2(x[2] * mul, x[3] * mul));
-  if (a.lse && lane == 0) a.lse[out_row] = sum > 0.0f ? (__log2f(sum) + top - 14.0f) * kLn2 : -INFINITY;
+  if (a.lse && lane == 0) a.lse[out_row] = sum != 0.0f ? (__log2f(sum) + top - 14.0f) * kLn2 : -INFINITY;
 }
 
 // Workgroups along the keys: enough to fill the chip, none with less than a
