@@ -445,6 +445,8 @@ typedef struct bl_kv_batch {
  *   round_half_even(fl32(value * fl32(127 / a))), and, where a > a_old, those
  *   already there become round_half_even(fl32(q * fl32(a_old / a)));
  * pages whose values all stay below 2^-64 are written as zeros with absmax 0.
+ * A NaN or an infinity becomes the absmax of its page and head, which then
+ * stands for NaN.
  * Writing the same tokens again gives the same cache.  A page that is written
  * must belong to one sequence of the batch only.
  *   k, v   bf16 [tokens][heads][dim], strides in elements (multiples of 8).

@@ -222,13 +222,15 @@ struct Rows {
   int64_t token, head;
 };
 
-__device__ __forceinline__ float block_max(float v, float* part, int threads) {
-  v = __int_as_float(wave_reduce<true>(__float_as_int(v)));  // v >= 0: its bits order like it
+// Magnitudes as bits, which order like the values, a NaN above them all: it
+// becomes the page's absmax instead of vanishing in a code.
+__device__ __forceinline__ int block_max(int v, int* part, int threads) {
+  v = wave_reduce<true>(v);
   if (threads > 64) {
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
     v = part[0];
-    for (int i = 1; i < threads / 64; ++i) v = fmaxf(v, part[i]);
+    for (int i = 1; i < threads / 64; ++i) v = max(v, part[i]);
   }
   return v;
 }
@@ -237,7 +239,7 @@ template <bool kVec, bool kInter, int T>
 __global__ __launch_bounds__(T) void k_kv_append(KvView kv, KvStep st, Rows k, Rows v, Head kh, Head vh,
                                                  const float* __restrict__ turns, float magnitude, int page_blocks,
                                                  Rows q, int q_heads, uint16_t* q_out) {
-  __shared__ float part[T / 64];
+  __shared__ int part[T / 64];
   constexpr int kHold = 1;
   const int s = blockIdx.y, tid = threadIdx.x;
   const int begin = st.begin(s), count = st.count(s, begin), start = st.start_of(s);
@@ -297,12 +299,13 @@ __global__ __launch_bounds__(T) void k_kv_append(KvView kv, KvStep st, Rows k, R
       turn_unit<kInter>(x, cs, sn);
     }
   };
-  auto top_of = [](const float(&x)[16], float top) {
+  auto top_of = [](const float(&x)[16], int top) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x[j]));
+    for (int j = 0; j < 16; ++j) top = max(top, __float_as_int(fabsf(x[j])));
     return top;
   };
-  float held[kHold][16], top = 0.0f;
+  float held[kHold][16];
+  int top = 0;
 #pragma unroll
   for (int i = 0; i < kHold; ++i) {
     fetch(tid + i * T, held[i]);
@@ -313,7 +316,7 @@ __global__ __launch_bounds__(T) void k_kv_append(KvView kv, KvStep st, Rows k, R
     fetch(item, x);
     top = top_of(x, top);
   }
-  float a = fmaxf(a_old, block_max(top, part, T));
+  float a = __int_as_float(max(__float_as_int(a_old), block_max(top, part, T)));
   if (a < 0x1p-64f) a = 0.0f;
   const float scale = a > 0.0f ? 127.0f / a : 0.0f;
   auto put = [&](int item, const float(&x)[16]) {
