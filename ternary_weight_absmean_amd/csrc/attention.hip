@@ -42,7 +42,9 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kStep = 64;       // keys per step of a wave
 constexpr float kLeastAbsmax = 0x1p-64f;
-constexpr float kNone = -1e30f;  // a running maximum that nothing has raised
+// A running maximum that nothing has raised: below every score (those that
+// overflow are not seen), finite so that differences of two are 0.
+constexpr float kNone = -0x1.fffffep127f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Attn {

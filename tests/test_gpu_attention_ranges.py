@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import _block
-from _gpu import say
+import ternary_weight_absmean_amd as bl
+from _gpu import DEV, bf16, bf16_bits_to_f64, host, say
 from test_gpu_attention import check
 from test_gpu_kv_cache import Case, heads
 
@@ -71,3 +72,30 @@ def test_only_pages_of_zero_values(ctx, new):
     c.v[:], c.va[:] = 0, 0
     say(f"bl_attention only zero pages, ctx={ctx} new={new}")
     assert not check(c, heads(rng, c.total, 2, 64)).any()
+
+
+@pytest.mark.parametrize("ctx,new", STEPS)
+@pytest.mark.parametrize("scale", [-1.0, -1e12, -1e30, -1e35, 1e30])
+def test_scores_far_below_zero(ctx, new, scale):
+    """One page is there, its keys along the queries: the one that scores highest (with a negative scale the
+    shortest) takes everything, the next being a tenth of the score away.  Its score is right to the query's
+    2^-15 and a few fp32 roundings."""
+    rng = np.random.default_rng(ctx)
+    c = Case(rng, [ctx], [new], 1, 64, 16)
+    one = heads(rng, 64)
+    top, p = np.abs(one).max(), c.table[0, 0]
+    c.k[p, 0] = np.rint(rng.permutation(np.arange(1, 17))[:, None] / 16 * one * (127 / top))
+    c.ka[p] = top
+    c.table[0, 1:] = -1
+    if scale == -1.0:
+        one = one * np.float32(2.0 ** 8)
+    q = np.broadcast_to(one, (c.total, 2, 64)).copy()
+    cache, batch = c.device()
+    lse = torch.full(q.shape[:2], 9.0, device=DEV)
+    say(f"bl_attention scores far below zero, ctx={ctx} new={new} scale={scale}")
+    out = bf16_bits_to_f64(host(bl.bl_attention(cache, batch, bf16(_block.bits(q)), scale=scale, lse=lse)))
+    score = scale * (c.k[p, 0].astype(np.float64) @ one) * float(c.ka[p, 0]) / 127
+    best = int(score.argmax())
+    want = c.v[p, 0, best].astype(np.float64) * float(c.va[p, 0]) / 127
+    assert (np.abs(out - want) <= np.abs(want) * (_block.U16 + 2.0 ** -10)).all()
+    assert (np.abs(host(lse) / score[best] - 1) <= 2.0 ** -12).all()
