@@ -362,7 +362,8 @@ bl_status bl_rmsnorm_backward(const float* dn, const uint16_t* r, const float* w
  * a and b being elements i and i + rot/2 (interleaved = 0) or 2i and 2i + 1
  * (interleaved = 1); elements from rot on pass unchanged.  f_i is held as
  * turns per position in two fp32 numbers (value and remainder), with which the
- * fraction of a turn is right to about 2^-23 for positions below 2^24. */
+ * fraction of a turn is right to about 2^-23 for positions below 2^24: cos and
+ * sin to 4e-7 in bf16 outputs, to 2^-23 in keys that bl_kv_append quantizes. */
 typedef struct bl_rope_table {
     const float* turns; /* device, [rot / 2][2] fp32, as bl_rope_frequencies fills it */
     int64_t rot;        /* even, 0 < rot <= head dimension                           */

@@ -4,9 +4,13 @@
 // A rotation by position * f is a rotation by the fraction of position * f / 2pi
 // turns.  The table holds f / 2pi as two fp32 (value and remainder): with
 // p = fl(pos * hi), e = fma(pos, hi, -p) is the product's exact error, so
-// frac(p) + (e + pos * lo) is the turn's fraction to about 2^-23 at every
-// position below 2^24, where a product of fp32 radians is off by pos * 2^-25.
-// v_sin_f32 and v_cos_f32 take turns.
+// the turn's fraction is p - round(p) plus e + pos * lo at every position below
+// 2^24, where a product of fp32 radians is off by pos * 2^-25.
+//
+// v_cos_f32 and v_sin_f32 of the turn are off by up to 2.7e-7 (4e-7 at the
+// farthest positions): nothing beside a rounding to bf16, which queries and bl_rope's outputs take.  Keys are
+// quantized from fp32, where such an error turns codes beside a rounding
+// boundary and moves a page's scale; theirs are right to 2^-23 (unit_angles).
 //
 // All three calls move bytes: 2 in and 2 out per rotated element; 2 in and 1
 // out per appended element, 1 in and 2 out per element read back.  HBM-bound
@@ -128,7 +132,13 @@ __device__ __forceinline__ void store_codes(const Head& h, int u, int8_t* row, c
 
 // cos and sin (times the magnitude; sin negated for the inverse) of the eight
 // pairs of unit u at position pos.
-template <bool kVec, bool kInter>
+// kFine: with q = round(4 t) for the turn t, x = t - q / 4 lies within an eighth
+// of a turn, where polynomials in x^2 (interpolated at Chebyshev nodes, off by
+// 3e-9 and 1e-10) give both; q's low bits exchange and negate them.  t is not
+// rounded on the way to x, so both are right to 2^-23 (1.2e-7 at most over 4
+// million angles).  For all rotations the prompts' rotation would take 31 us
+// instead of 28 and the prompts' cache 63 instead of 59; for the keys alone it is 61.
+template <bool kVec, bool kInter, bool kFine>
 __device__ __forceinline__ void unit_angles(const Head& h, int u, const float* turns, float pos, float magnitude,
                                             float sign, float (&cs)[8], float (&sn)[8]) {
   float f[16];
@@ -150,10 +160,27 @@ __device__ __forceinline__ void unit_angles(const Head& h, int u, const float* t
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float p = pos * f[2 * j];
-    const float e = __builtin_fmaf(pos, f[2 * j], -p);
-    const float turn = __builtin_amdgcn_fractf(p) + __builtin_fmaf(pos, f[2 * j + 1], e);
-    cs[j] = __builtin_amdgcn_cosf(turn) * magnitude;
-    sn[j] = __builtin_amdgcn_sinf(turn) * (magnitude * sign);
+    const float rest = __builtin_fmaf(pos, f[2 * j + 1], __builtin_fmaf(pos, f[2 * j], -p));
+    if (kFine) {
+      const float near = p - rintf(p);
+      const float q = rintf((near + rest) * 4.0f);
+      const float x = __builtin_fmaf(q, -0.25f, near) + rest, u = x * x;
+      float s = __builtin_fmaf(-75.401611328125f, u, 81.59254455566406f);
+      s = __builtin_fmaf(s, u, -41.3416633605957f);
+      s = __builtin_fmaf(s, u, 6.2831854820251465f) * x;
+      float c = __builtin_fmaf(59.42410659790039f, u, -85.44882202148438f);
+      c = __builtin_fmaf(c, u, 64.93936920166016f);
+      c = __builtin_fmaf(c, u, -19.739208221435547f);
+      c = __builtin_fmaf(c, u, 1.0f);
+      const uint32_t quarter = (uint32_t)(int)q;
+      const uint32_t flip_s = quarter << 30 & 0x80000000u, flip_c = (quarter + 1) << 30 & 0x80000000u;
+      cs[j] = __uint_as_float(__float_as_uint(quarter & 1 ? s : c) ^ flip_c) * magnitude;
+      sn[j] = __uint_as_float(__float_as_uint(quarter & 1 ? c : s) ^ flip_s) * (magnitude * sign);
+    } else {
+      const float turn = __builtin_amdgcn_fractf(p) + rest;
+      cs[j] = __builtin_amdgcn_cosf(turn) * magnitude;
+      sn[j] = __builtin_amdgcn_sinf(turn) * (magnitude * sign);
+    }
   }
 }
 
@@ -198,7 +225,7 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(const uint16_t* x, int64_
   load_unit<kVec, kInter>(h, u, x + (int64_t)token * xt + head * xh, v);
   if (u < h.turning) {
     float cs[8], sn[8];
-    unit_angles<kVec, kInter>(h, u, turns, (float)position[token], magnitude, sign, cs, sn);
+    unit_angles<kVec, kInter, false>(h, u, turns, (float)position[token], magnitude, sign, cs, sn);
     turn_unit<kInter>(v, cs, sn);
   }
   store_unit<kVec, kInter, true>(h, u, y + (int64_t)token * yt + head * yh, v);
@@ -255,7 +282,7 @@ __global__ __launch_bounds__(T) void k_kv_append(KvView kv, KvStep st, Rows k, R
     load_unit<kVec, kInter>(kh, u, q.p + token * q.token + head * q.head, x);
     if (u < kh.turning) {
       float cs[8], sn[8];
-      unit_angles<kVec, kInter>(kh, u, turns, (float)((int64_t)start + i), magnitude, 1.0f, cs, sn);
+      unit_angles<kVec, kInter, false>(kh, u, turns, (float)((int64_t)start + i), magnitude, 1.0f, cs, sn);
       turn_unit<kInter>(x, cs, sn);
     }
     store_unit<kVec, kInter, T != 64>(kh, u, q_out + (token * q_heads + head) * kh.dim, x);
@@ -295,7 +322,7 @@ __global__ __launch_bounds__(T) void k_kv_append(KvView kv, KvStep st, Rows k, R
     load_unit<kVec, kInter>(h, u, from, x);
     if (u < h.turning) {
       float cs[8], sn[8];
-      unit_angles<kVec, kInter>(h, u, turns, (float)(first + keep + row), magnitude, 1.0f, cs, sn);
+      unit_angles<kVec, kInter, true>(h, u, turns, (float)(first + keep + row), magnitude, 1.0f, cs, sn);
       turn_unit<kInter>(x, cs, sn);
     }
   };
