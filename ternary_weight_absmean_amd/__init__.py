@@ -468,7 +468,8 @@ def _heads(t: torch.Tensor, name: str, shape: tuple) -> tuple[int, int, int]:
     token, head, one = t.stride()
     if one != 1 and shape[2] > 1:
         raise ValueError(f"the last axis of {name} must be contiguous")
-    return t.data_ptr(), token, head
+    # the stride of an axis of one element is any number, and not used
+    return t.data_ptr(), 0 if shape[0] == 1 else token, 0 if shape[1] == 1 else head
 
 
 def bl_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: torch.Tensor | None = None,

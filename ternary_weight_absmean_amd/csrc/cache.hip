@@ -8,9 +8,10 @@
 // 2^24, where a product of fp32 radians is off by pos * 2^-25.
 //
 // v_cos_f32 and v_sin_f32 of the turn are off by up to 2.7e-7 (4e-7 at the
-// farthest positions): nothing beside a rounding to bf16, which queries and bl_rope's outputs take.  Keys are
-// quantized from fp32, where such an error turns codes beside a rounding
-// boundary and moves a page's scale; theirs are right to 2^-23 (unit_angles).
+// farthest positions): nothing beside a rounding to bf16, which queries and
+// bl_rope's outputs take.  Keys are quantized from fp32, where such an error
+// turns codes beside a rounding boundary and moves a page's scale; theirs are
+// right to 2^-23 (unit_angles).
 //
 // All three calls move bytes: 2 in and 2 out per rotated element; 2 in and 1
 // out per appended element, 1 in and 2 out per element read back.  HBM-bound
