@@ -602,7 +602,8 @@ class KVCache:
 class KVBatch:
     """The tokens of one step: int32 device tensors ``page_table`` [seqs][stride], ``start`` [seqs] (tokens that
     each sequence had before) and ``offsets`` [seqs + 1] (where its new tokens begin among the step's ``tokens``);
-    ``max_new`` and ``max_len`` bound a sequence's new tokens and its length with them."""
+    ``max_new`` and ``max_len`` bound a sequence's new tokens and its length with them (attention sees no position
+    from ``max_len`` on)."""
 
     class _Struct(ctypes.Structure):
         _fields_ = [("page_table", _P), ("start", _P), ("offsets", _P), ("seqs", _I64), ("table_stride", _I64),

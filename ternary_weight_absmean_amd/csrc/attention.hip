@@ -247,7 +247,7 @@ constexpr float kSlack = 1.5f;
 // that loads are in flight nearly all the time without a second set of
 // registers (three waves per SIMD, 16 KB in flight each).  HBM-bound: 24
 // sequences of up to 32768 tokens, 64/8 heads of 128 (883 MB): 160 us, 5.5 TB/s,
-// and 9 us for the join; one token over 1500 (20/5 heads): 7.6 + 4 us, the
+// and 9 us for the join; one token over 1500 (20/5 heads): 7.3 + 4.4 us, the
 // chain of page number, keys, products, meeting of the waves, join.
 // kPages: pages that 64 tokens lie in (1, or 4 for pages of 16 and
 // 32 tokens, looked up for each 16 tokens).
@@ -510,8 +510,9 @@ __global__ __launch_bounds__(kThreads, DC == 1 ? 4 : DC == 2 ? (kPages == 1 ? 3 
 // instructions, 16 of which (the exponentials) take two turns, against 16 MFMAs
 // of 32 cycles, and each MFMA takes two to three turns of issue itself.
 // 24000 tokens of 20/5 heads of 128: 920 TFLOP/s (a bf16 library product of 8192
-// cubed reaches 1217); 6000 tokens: 220 us, 837 TFLOP/s, where the longest tiles
-// (94 steps) set the end.
+// cubed reaches 1217); 6000 tokens: 221 us, 833 TFLOP/s, where the longest tiles
+// (94 steps) set the end.  Figures with steady clocks: the first calls after a
+// pause, some 30 ms of them, take up to a quarter longer.
 // One team of four waves takes all steps, two workgroups to a CU; or two teams
 // take them in turn, each with its own running state and buffers, one workgroup
 // to a CU, and are joined in LDS at the end (see make_plan for which).
@@ -686,8 +687,8 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
   // waves alone on a SIMD the one hides the other's products only in part (16
   // products and their softmax in turn 883 cycles, mixed 693).  Wave priorities:
   // staging, which other waves wait for, before the values' products before the
-  // rest (6000 tokens, 20/5 heads: 267 us against 283 without; 512 rows of a
-  // window of 1024 54.8 against 56.9).
+  // rest (6000 tokens, 20/5 heads: 223 us against 245 without; 6 x 509 under a
+  // window of 1024 52.7 against 55.8).
   v16i high, lo;   // the next half's scores
   v8h pf[2];       // the half before: its probabilities,
   uint4 vf[2][kTiles];  // and its values
@@ -974,11 +975,11 @@ struct Plan {
 // Workgroups of 16 rows (k_attn) or of 128 (k_attn_prompt).  The former read
 // and convert the keys and values once per 16 rows, but their four waves share
 // a tile's steps, so that few rows, and many over few keys, are done sooner:
-// 25 x 1200 rows of 64 over up to 600 keys 14 us against 16, 5 x 2800 of 128 over
-// 700 19 against 23, 15 x 400 over 900 15 against 24; but 40 x 1200 of 64 18
-// against 16, 40 x 512 of 128 over 640 26 against 21, 28 x 2644 over 721 50 against
-// 32, and 64 tokens of 20 heads over 4064 keys 31 against 25.  Between 16000 and
-// 30000 tile steps either may win, by 15 %.
+// 5 x 2800 rows of 128 over up to 700 keys 20 us against 22, 15 x 400 over 900 16
+// against 23; but 28 x 2644 over 721 56 against 31, and 64 tokens of 20 heads over
+// 4064 keys 30 against 24.  Between 16000 and 25000 tile steps either may win: 25
+// x 1200 rows of 64 over 600 keys (16900) 15 us against 14, 40 x 512 of 128 over
+// 600 (23000) 26 against 20.
 bool few_rows(int64_t rows, int64_t lists, int64_t steps, int dim) {
   const int64_t tiles = lists * ((rows + 15) / 16), chunks = (dim + 63) / 64;
   return rows < 64 || (steps <= 32 && tiles * steps * chunks < 25000);
@@ -986,10 +987,10 @@ bool few_rows(int64_t rows, int64_t lists, int64_t steps, int dim) {
 
 // Two teams (one workgroup of eight waves to a CU) while the tiles fill the
 // 256 CUs less than twice and have many steps: a tile then takes half the
-// time (470 tiles of up to 47 steps: 82 us against 99 with one team, 256 of 47: 58
-// against 76, 235 of 24: 39 against 51).  One team (two independent workgroups to
-// a CU) where there are tiles enough (940 of up to 94: 245 us against 263) or,
-// past one per CU, few steps (480 of 20: 55 against 64).
+// time (470 tiles of up to 47 steps: 73 us against 91 with one team, 256 of 47: 61
+// against 78, 235 of 24: 37 against 49).  One team (two independent workgroups to
+// a CU) where there are tiles enough (940 of up to 94: 223 us against 240) or,
+// past one per CU, few steps (480 of 20: 53 against 61).
 bool two_teams(int dim, int64_t tiles, int64_t steps) {
   return dim <= 128 && ((tiles < 256 && steps > 6) || (tiles < 512 && steps > 24));
 }
@@ -1015,11 +1016,11 @@ Plan make_plan(const KvView& kv, int64_t seqs, int64_t max_new, int64_t max_len,
     return wanted < most ? wanted : most;
   };
   // Up to this many steps a split gives less than the join and its launch take
-  // (steps of 128 elements, one workgroup against splits: 12 steps 9.5 us against
-  // 10.6, 16 10.5 against 10.6, 24 13.1 against 10.9; 320 tiles of 16 18.7 against
-  // 21.4).  Longer heads' steps take longer, which a few tiles' own time shows
-  // (256 elements, 5 tiles of 16 steps 16.7 against 13.0, 80 of 11 16.8 against
-  // 14.9; but 320 of 10 26 against 36).
+  // (steps of 128 elements, one workgroup against splits: 12 steps 9.0 us against
+  // 10.2, 16 10.6 against 10.0, 24 14.0 against 10.7; 320 tiles of 16 18.7 against
+  // 21.6).  Longer heads' steps take longer, which a few tiles' own time shows
+  // (256 elements, 5 tiles of 16 steps 19.9 against 12.9, 80 of 11 16.8 against
+  // 15.0; but 320 of 10 27 against 37).
   const int64_t unsplit = p.tile_rows == 16 && kv.dim > 128 && p.tiles < 160 ? kUnsplit / 2 : kUnsplit;
   int64_t splits = 1;
   if (steps <= unsplit) {

@@ -31,7 +31,9 @@ namespace {
 //   copied: runs at rot + 8(u - R) and as many units further.
 // Otherwise the runs of a turned unit are at 8u and rot/2 + 8u, or 16u and
 // 16u + 8, and those of a copied one at rot + 16(u - R) and 8 further, element
-// by element.  A thread owns its unit's elements, so a rotation in place is safe.
+// by element (4099 tokens of 72 heads of 128: 132 us with 40 elements turned, 117
+// with 72, 25 with 128).  A thread owns its unit's elements, so a rotation in
+// place is safe.
 struct Head {
   int dim, rot, half, turning, units;  // turning = R
 };
@@ -204,10 +206,12 @@ __device__ __forceinline__ void turn_unit(float (&v)[16], const float (&cs)[8], 
 // ---- bl_rope ----
 // One thread per unit of a head (unit fastest, then head, then token).  Several
 // heads per thread would share the angles, but take registers from the waves
-// that hide the loads: 4099 tokens of 72 heads of 128 (151 MB) take 31 us with
-// one head per thread, 34 with two, 37 with four.  Stores go past the caches, so
-// that they keep the inputs of earlier kernels instead: 30 us against 35 (three
-// quarters of each head turned).
+// that hide the loads: 4099 tokens of 72 heads of 128 (151 MB) took 31 us with
+// one head per thread, 34 with two, 37 with four.  Stores go past the caches,
+// which then keep the inputs of kernels before instead: 27 us against 32 for that
+// size, three quarters of each head turned, three sets of inputs in turn.  The
+// other side is a next kernel that reads the result at once (52 us for both
+// against 47; 2048 tokens of 25 heads 12 either way).
 constexpr int kRopeThreads = 256;
 
 template <bool kVec, bool kInter>
@@ -238,13 +242,14 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(const uint16_t* x, int64_
 // (rotated in fp32), then codes.  A thread's first unit stays in registers
 // between the two steps, further ones are read again (from L2), which costs
 // less than the registers: 5 prompts of up to 1777 tokens (64 + 2 x 8 heads of
-// 128, 227 MB) take 50 us (4.5 TB/s) with one unit held, 52 with two; the
+// 128, 227 MB) take 51 us (4.5 TB/s) with one unit held, 53 with two; the
 // queries' rotation, most of their bytes, hides the pages' loads and is no
 // faster in a launch of its own (40 + 16 us).  64 sequences' single tokens of
 // 20 + 2 x 5 heads take 4 us, a launch and its dependent loads (page number,
 // absmax).  A prompt's queries are stored past the caches like k_rope's outputs
-// (61 us against 63 with the read back; the decoder example's pass is the
-// same), a decoded token's are left in them for the attention.
+// (58 us against 60 with the read back; with the attention over the same prompts
+// next 244 against 240; the decoder example's pass is the same), a decoded token's
+// are left in them for the attention.
 struct Rows {
   const uint16_t* p;
   int64_t token, head;
@@ -385,7 +390,8 @@ __global__ __launch_bounds__(T) void k_kv_append(KvView kv, KvStep st, Rows k, R
 
 // ---- bl_kv_read ----
 // One thread per 16 codes of a token's head (chunk fastest); y = sequence, z = k
-// or v.  36 MB (a third in, two thirds out) in 10 us.
+// or v.  36 MB (a third in, two thirds out) in 10 us: three dependent loads
+// (lengths, page number, codes and scale) for one 16-byte piece of a thread.
 constexpr int kReadThreads = 256;
 
 __global__ __launch_bounds__(kReadThreads) void k_kv_read(KvView kv, KvStep st, uint16_t* __restrict__ k,

@@ -33,11 +33,13 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&f)[8]) {
 // zeros has without an eps: its norm is zeros and it adds nothing to a gradient.
 __device__ __forceinline__ float rsqrt_or_zero(float v) { return v == 0.0f ? 0.0f : 1.0f / sqrtf(v); }
 
-// A store that leaves the caches to others: the sum and the bf16 outputs are
-// not what the next kernel reads (that is xq), and by the time of their own next
-// use other kernels have passed.  2048 x 8192 with residual: 23 us against 31
-// (the inputs of earlier kernels stay in the Infinity Cache); a block of the
-// decoder example takes the same 504 us per prompt pass either way.
+// A store that leaves the caches to others.  2048 x 8192 with residual and three
+// sets of inputs in turn: 23 us against 31, because those stay in the Infinity
+// Cache; a block of the decoder example takes the same 504 us per prompt pass
+// either way.  The sum and xhat are read only after other kernels have passed.
+// Where y is the only output the next kernel does read it, and loses nothing by
+// it (norm and a reader: 4 x 2560 4.1 us either way, 2048 x 2560 8.5 against 8.9,
+// 2048 x 8192 20.5 both).
 __device__ __forceinline__ void store_past_caches(uint4* p, const uint4& v) {
   typedef unsigned v4u __attribute__((ext_vector_type(4)));
   __builtin_nontemporal_store((v4u){v.x, v.y, v.z, v.w}, reinterpret_cast<v4u*>(p));
@@ -175,8 +177,8 @@ __global__ __launch_bounds__(T) void k_rmsnorm_quant(const uint4* x, const uint4
 // workgroups' sums go to the workspace and a second kernel adds them in a
 // fixed order, so no atomics and the same bits every time.  HBM-bound: 4096 x
 // 8192 with dr (336 MB, and 8 MB of partial sums written and read again) 65 us,
-// 5.2 TB/s; 333 x 6912 11.1 us, one or two rows per workgroup, so two round trips
-// and a reduction in each kernel.
+// 5.2 TB/s; 333 x 6912 11 us (8.4 + 3.3): 77 of 256 workgroups take a second row,
+// with its own round trip and reduction, and each writes 28 KB of partial sums.
 template <int T, int kC>
 __global__ __launch_bounds__(T) void k_rmsnorm_backward(const uint4* __restrict__ dn, const uint4* __restrict__ r,
                                                         const uint4* __restrict__ w, const uint4* dr, int64_t m, int k8,
