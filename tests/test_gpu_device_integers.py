@@ -147,3 +147,44 @@ def test_cache_calls_with_integers_out_of_range(start, offsets):
         np.testing.assert_array_equal(got[0:inside[0]], _block.bits(back[:inside[0]]))
         np.testing.assert_array_equal(got[20:20 + inside[1]], _block.bits(back[inside[0]:]))
         assert (got[inside[0]:20] & 0x7FFF == 0).all() and (got[20 + inside[1]:] & 0x7FFF == 0).all()
+
+
+def test_captured_step_replayed_past_its_table():
+    """A graph that moves its own positions, replayed past max_len: the same as eager calls at those positions, the
+    bytes around the cache and the workspace as they were."""
+    rng = np.random.default_rng(17)
+    c = Case(rng, [1010, 500], [1, 1], 2, 64, 16)
+    assert c.table.shape[1] * 16 == 1024  # the positions of the table; the second sequence's pages end at 512
+
+    def fresh():
+        k, v, ka, va = (Walled(a.shape, t, torch.from_numpy(a)) for a, t in (
+            (c.k, torch.int8), (c.v, torch.int8), (c.ka, torch.float32), (c.va, torch.float32)))
+        start = i32([1010, 500])
+        batch = bl.KVBatch(i32(c.table), start, i32([0, 1, 2]), 2, 1, 1024)
+        cache = bl.KVCache(k.t, v.t, ka.t, va.t)
+        ws = Walled((max(16, bl.bl_attention_workspace_bytes(cache, batch, 4)),), torch.uint8)
+        out, q_out = (torch.zeros((2, 4, 64), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        return cache, batch, start, (k, v, ka, va, ws), out, q_out
+
+    qkv = bf16(_block.bits(heads(rng, 2, 8, 64)))
+    rope = bl.Rope(bl.bl_rope_frequencies(64).to(DEV))
+
+    def step(cache, batch, start, walls, out, q_out):
+        bl.bl_kv_append(cache, batch, qkv[:, 4:6], qkv[:, 6:], rope=rope, q=qkv[:, :4], q_out=q_out)
+        bl.bl_attention(cache, batch, q_out, out=out, workspace=walls[4].t)
+        start.add_(1)
+
+    say("captured step replayed past its table")
+    eager, captured = fresh(), fresh()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(*captured)
+    for i in range(20):  # positions 1010 .. 1029: the last six are past the table
+        step(*eager)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(captured[4], eager[4]) and torch.isfinite(captured[4].float()).all(), f"replay {i}"
+    for a, b in zip(captured[3][:4], eager[3][:4]):
+        assert a.intact() and b.intact() and torch.equal(a.t, b.t)
+    assert captured[3][4].intact() and eager[3][4].intact()
