@@ -328,8 +328,8 @@ bl_status bl_unpack_ternary(const uint8_t* packed, int64_t n, int64_t k, int8_t*
  *   xq, alpha    out [m][k] int8 and [m] fp32, both or neither NULL.
  * At least one output is required.  k is a multiple of 64, at most
  * BL_MAX_NORM_K (a row stays in registers); |h| below 2^56, so that the sum of
- * squares is finite, and, where eps is 0, mean h^2 no fp32 denormal.  x, residual, weight and the [m][k] outputs are 16-byte
- * aligned.
+ * squares is finite, and, where eps is 0, mean h^2 no fp32 denormal.  x,
+ * residual, weight and the [m][k] outputs are 16-byte aligned.
  * Errors: BL_ERR_NULL, BL_ERR_SHAPE (also a bad eps), BL_ERR_ALIGN, BL_ERR_HIP. */
 #define BL_MAX_NORM_K 32768
 bl_status bl_rmsnorm_quant(const uint16_t* x, const uint16_t* residual, const float* weight, int64_t m, int64_t k,
