@@ -444,7 +444,7 @@ def _plain_compact(st, c):
     used = refs > 0
     count = int(used.sum())
     to = torch.nonzero(~used[:count])[:, 0]
-    source = torch.nonzero(used[count:])[:, 0] + count
+    source = torch.nonzero(used[count:])[:, 0].flip(0) + count  # the highest first
     moved = min(to.numel(), st["moves"])
     to, source = to[:moved], source[:moved]
     name = torch.arange(refs.numel(), device=DEV)
@@ -606,7 +606,7 @@ def _exact_compact(st, c):
     rows = [r[:-(-n // page)] for r, n in zip(st["table0"].tolist(), keep)]
     pages = len(st["refs0"])
     held = {p for r in rows for p in r}
-    above, below = sorted(p for p in held if p >= len(held)), [p for p in range(len(held)) if p not in held]
+    above, below = sorted((p for p in held if p >= len(held)), reverse=True), [p for p in range(len(held)) if p not in held]
     copies = [(a, b, page) for a, b in zip(above, below)]
     name = {a: b for a, b, _ in copies}
     rows = [[name.get(p, p) for p in r] for r in rows]
