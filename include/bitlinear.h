@@ -494,6 +494,143 @@ bl_status bl_attention(const bl_kv_cache* cache, const bl_kv_batch* batch, const
                        int64_t q_head_stride, int64_t q_heads, float scale, int64_t window, int64_t sinks,
                        uint16_t* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Many answers to one prompt: pages of the cache ----
+ * refs[p] counts the entries of page tables that hold page p; 0: the page is
+ * free.  Sequences that begin alike may hold the same pages there (bl_kv_fork);
+ * a page that is written (bl_kv_append) belongs to one sequence.  A new pool is all zeros.
+ * One pool serves the caches of all blocks, which use the same page numbers.
+ * A page number outside 0 .. pages - 1 in a table marks an entry without a
+ * page (the calls below write -1).
+ * Pages are handed out lowest number first, to requests in the order of
+ * sequences and, within one, of positions: equal inputs give equal results.
+ * shortage: NULL, or a device integer to which the number of requests that
+ * found no free page is added (their entries stay, or become, -1); the host
+ * clears it.  Counts that do not agree with the tables give no access outside
+ * a buffer; no count goes below 0. */
+#define BL_MAX_POOL_PAGES (1 << 24)
+#define BL_MAX_FORK_SEQS 8192
+typedef struct bl_kv_pool {
+    int32_t* refs;       /* device [pages], 16-byte aligned    */
+    int64_t pages;       /* 1 .. BL_MAX_POOL_PAGES             */
+    int32_t page_tokens; /* tokens per page, as in the caches  */
+} bl_kv_pool;
+
+/* Gives pages to the entries without one in which the batch's new tokens
+ * stand (positions start[s] .. start[s] + offsets[s + 1] - offsets[s] - 1):
+ * call it before bl_kv_append.  page_table is written; entries past
+ * table_stride get none and are not counted as a shortage.
+ *   copies  NULL, or out device [seqs][3] for bl_kv_copy: a part-filled page in
+ *           which a sequence goes on writing (position start[s]) and that others
+ *           hold too is copied onto a fresh one, {source, target, tokens},
+ *           {-1, -1, 0} elsewhere; of sequences of the batch that share it, the
+ *           last one keeps it if nobody else does.  Such pages come from
+ *           cutting back (bl_kv_free with keep) into pages that a fork shares.
+ * Errors: BL_ERR_NULL, BL_ERR_SHAPE (also when sequences times the pages that
+ * max_new tokens may enter pass 2^24), BL_ERR_ALIGN, BL_ERR_HIP. */
+bl_status bl_kv_grow(const bl_kv_pool* pool, const bl_kv_batch* batch, int32_t* copies, int32_t* shortage, void* stream);
+
+/* Forks sequences: child c continues parent p = parent[c], which holds
+ * length[p] tokens (taken as 0 .. table_stride * page_tokens).  The child
+ * shares the parent's full pages; the last, part-filled one is copied onto a
+ * fresh page: copies[c] = {source, target, tokens} for bl_kv_copy, {-1, -1, 0}
+ * where nothing is to be copied.  Entries past length[p] are -1.  A parent[c]
+ * outside 0 .. seqs - 1 makes an empty child: no page, length 0.
+ *   keep_parents  non-zero: the parents keep their rows and pages.  0: they are
+ *                 given up (beams): the first child of a parent takes its
+ *                 part-filled page over as it is, and pages that no child holds
+ *                 become free once the call is done (it hands out none of them
+ *                 itself).  `table` is not changed, its rows mean nothing then.
+ *   table         device [seqs][table_stride]; length device [seqs].
+ *   parent        device [children].
+ *   table_out     out device [children][table_stride], not `table`.
+ *   length_out    out device [children]: the parents' lengths.
+ *   copies        out device [children][3].
+ * seqs and children are at most BL_MAX_FORK_SEQS.
+ * Errors: BL_ERR_NULL, BL_ERR_SHAPE (also table_out = table), BL_ERR_ALIGN, BL_ERR_HIP. */
+bl_status bl_kv_fork(const bl_kv_pool* pool, const int32_t* table, int64_t table_stride, const int32_t* length,
+                     int64_t seqs, const int32_t* parent, int64_t children, int keep_parents, int32_t* table_out,
+                     int32_t* length_out, int32_t* copies, int32_t* shortage, void* stream);
+
+/* Gives pages back: row s of table keeps those of its first keep[s] tokens
+ * (none if keep is NULL or keep[s] < 1), the entries past them become -1 and
+ * their pages lose a holder.
+ *   table  device [seqs][table_stride]; keep device [seqs] or NULL.
+ * Errors: BL_ERR_NULL, BL_ERR_SHAPE, BL_ERR_ALIGN, BL_ERR_HIP. */
+bl_status bl_kv_free(const bl_kv_pool* pool, int32_t* table, int64_t table_stride, int64_t seqs, const int32_t* keep,
+                     void* stream);
+
+/* Device workspace of bl_kv_compact (0: an argument is invalid). */
+size_t bl_kv_compact_workspace_bytes(const bl_kv_pool* pool, int64_t moves);
+
+/* Moves used pages to the front: with n pages in use, the highest used page
+ * goes to the lowest free one below n, the second highest to the second lowest
+ * and so on, at most `moves` of them (0 .. pages); then refs and the entries of table are
+ * changed accordingly.  After as many moves as there are, pages 0 .. n - 1
+ * are in use and the rest is free.  The codes are moved by bl_kv_copy with
+ * copies and moved, before the next call that writes a cache.
+ *   table   device [seqs][table_stride]: every row that holds pages of the pool.
+ *   copies  out device [moves][3]: {source, target, page_tokens}, then {-1, -1, 0}.
+ *   moved   out device [1]: how many there are.
+ * Errors: BL_ERR_NULL, BL_ERR_SHAPE, BL_ERR_ALIGN, BL_ERR_WORKSPACE, BL_ERR_HIP. */
+bl_status bl_kv_compact(const bl_kv_pool* pool, int32_t* table, int64_t table_stride, int64_t seqs, int64_t moves,
+                        int32_t* copies, int32_t* moved, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Copies pages inside each of `count` caches (one per block of a model, all of
+ * one shape): for every {source, target, tokens} of copies the codes of the
+ * first `tokens` tokens of all heads (at most page_tokens) and the scales; the
+ * target's other tokens stay as they are and mean nothing.  Entries whose
+ * pages are not there, or that have no tokens, are skipped.  The copies are
+ * made at once: no target is a source or another target.
+ *   caches  host array; copies device [n][3];
+ *   valid   NULL, or a device integer: only that many entries are looked at.
+ * Errors: BL_ERR_NULL, BL_ERR_SHAPE (also caches of different shapes), BL_ERR_ALIGN, BL_ERR_HIP. */
+bl_status bl_kv_copy(const bl_kv_cache* caches, int64_t count, const int32_t* copies, int64_t n, const int32_t* valid,
+                     void* stream);
+
+/* ---- Log probabilities ----
+ * Of the rows of logits x [m][n], with z_j = scale * x_j:
+ *   lse = log sum_j exp z_j,   logprob = z_t - lse  for the given token t,
+ *   entropy = -sum_j p_j log p_j,  p_j = exp(z_j - lse),
+ *   top_id, top_logprob: the `top` largest logits and their log
+ *   probabilities, in descending order, equal ones by ascending index.
+ * A logit of -infinity is a token that cannot occur: its p is 0, it is no
+ * alternative.  Where fewer than `top` tokens can occur, the rest of the row
+ * is -1 and -infinity.  Where none can, lse and logprob are -infinity and the
+ * entropy is 0.  A target outside 0 .. n - 1 has logprob 0 and no gradient.  A
+ * row that holds a NaN or +infinity gives NaN, NaNs are no alternatives.
+ * Statistics and sums are fp32; products scale * x must be finite where x is. */
+#define BL_MAX_VOCABULARY (1 << 20)
+#define BL_MAX_TOP 64
+enum { BL_BF16 = 0, BL_FP32 = 1 };
+
+/* Device workspace of bl_logprobs (0: none is needed, or an argument is invalid). */
+size_t bl_logprobs_workspace_bytes(int64_t m, int64_t n, int type, int64_t top);
+
+/*   x        [m][n] bf16 or fp32 (type), rows row_stride elements apart (>= n); aligned to its elements only.
+ *   scale    > 0, finite: 1 / temperature.
+ *   target   [m] int32, needed for logprob only.
+ *   logprob, lse, entropy  out fp32 [m], each NULL to skip it.
+ *   top      0 .. BL_MAX_TOP; top_id out int32 [m][top], top_logprob out fp32 [m][top].
+ * At least one output is required; n is at most BL_MAX_VOCABULARY.
+ * Results do not depend on the order in which workgroups run.
+ * Errors: BL_ERR_NULL, BL_ERR_SHAPE (also a bad type or scale), BL_ERR_ALIGN, BL_ERR_WORKSPACE, BL_ERR_HIP. */
+bl_status bl_logprobs(const void* x, int type, int64_t m, int64_t n, int64_t row_stride, float scale,
+                      const int32_t* target, int64_t top, float* logprob, float* lse, float* entropy, int32_t* top_id,
+                      float* top_logprob, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of sum_i (dlogprob_i logprob_i + dentropy_i entropy_i + dlse_i lse_i):
+ *   dx_j = scale * (dlogprob ([j = t] - p_j) + dlse p_j - dentropy p_j (log p_j + entropy)),
+ * from the logits and the lse and entropy that bl_logprobs gave for them.
+ *   dlogprob (with target), dentropy (with entropy), dlse  fp32 [m], each NULL
+ *            for zeros, not all.  A row whose gradients are all zero (or where
+ *            no token can occur) gets zeros whatever its logits are.
+ *   dx       out [m][n] of x's type, rows dx_stride elements apart; may be x
+ *            (with dx_stride = row_stride).  Between rows nothing is written.
+ * Errors: BL_ERR_NULL, BL_ERR_SHAPE, BL_ERR_ALIGN, BL_ERR_HIP. */
+bl_status bl_logprobs_backward(const void* x, int type, int64_t m, int64_t n, int64_t row_stride, float scale,
+                               const int32_t* target, const float* lse, const float* entropy, const float* dlogprob,
+                               const float* dentropy, const float* dlse, void* dx, int64_t dx_stride, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* bl_status_string(bl_status s);
 

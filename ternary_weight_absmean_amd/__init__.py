@@ -26,6 +26,8 @@ __all__ = [
     "bl_packed_bytes_b3", "bl_ternarize_pack_b3", "bl_bitlinear_b3",
     "bl_rmsnorm_quant", "bl_rmsnorm_backward_workspace_bytes", "bl_rmsnorm_backward", "bl_rope_frequencies", "bl_rope",
     "Rope", "KVCache", "KVBatch", "bl_kv_append", "bl_kv_read", "bl_attention_workspace_bytes", "bl_attention",
+    "KVPool", "KVCaches", "bl_kv_grow", "bl_kv_fork", "bl_kv_free", "bl_kv_compact_workspace_bytes", "bl_kv_compact",
+    "bl_kv_copy", "bl_logprobs_workspace_bytes", "bl_logprobs", "bl_logprobs_backward",
 ]
 
 
@@ -100,6 +102,24 @@ _lib.bl_attention_workspace_bytes.argtypes = [_P, _P, _I64]
 _lib.bl_attention_workspace_bytes.restype = _SZ
 _lib.bl_attention.argtypes = [_P, _P, _P, _I64, _I64, _I64, _F32, _I64, _I64, _P, _P, _P, _SZ, _P]
 _lib.bl_attention.restype = _INT
+_lib.bl_kv_grow.argtypes = [_P, _P, _P, _P, _P]
+_lib.bl_kv_grow.restype = _INT
+_lib.bl_kv_fork.argtypes = [_P, _P, _I64, _P, _I64, _P, _I64, _INT, _P, _P, _P, _P, _P]
+_lib.bl_kv_fork.restype = _INT
+_lib.bl_kv_free.argtypes = [_P, _P, _I64, _I64, _P, _P]
+_lib.bl_kv_free.restype = _INT
+_lib.bl_kv_compact_workspace_bytes.argtypes = [_P, _I64]
+_lib.bl_kv_compact_workspace_bytes.restype = _SZ
+_lib.bl_kv_compact.argtypes = [_P, _P, _I64, _I64, _I64, _P, _P, _P, _SZ, _P]
+_lib.bl_kv_compact.restype = _INT
+_lib.bl_kv_copy.argtypes = [_P, _I64, _P, _I64, _P, _P]
+_lib.bl_kv_copy.restype = _INT
+_lib.bl_logprobs_workspace_bytes.argtypes = [_I64, _I64, _INT, _I64]
+_lib.bl_logprobs_workspace_bytes.restype = _SZ
+_lib.bl_logprobs.argtypes = [_P, _INT, _I64, _I64, _I64, _F32, _P, _I64, _P, _P, _P, _P, _P, _P, _SZ, _P]
+_lib.bl_logprobs.restype = _INT
+_lib.bl_logprobs_backward.argtypes = [_P, _INT, _I64, _I64, _I64, _F32, _P, _P, _P, _P, _P, _P, _P, _I64, _P]
+_lib.bl_logprobs_backward.restype = _INT
 _lib.bl_status_string.argtypes = [ctypes.c_int]
 _lib.bl_status_string.restype = ctypes.c_char_p
 
@@ -684,3 +704,199 @@ def bl_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, scale: float |
                                              _dense(lse, "lse", torch.float32, shape[:2]), workspace.data_ptr(), _bytes(workspace),
                                              _stream(q.device)))
     return out
+
+
+# ---- many answers to one prompt ----
+
+class KVPool:
+    """Pages of the caches of a model: int32 ``refs`` [pages] on the device, how many page-table entries hold each
+    page (0: free).  Holds the tensor that it is given."""
+
+    class _Struct(ctypes.Structure):
+        _fields_ = [("refs", _P), ("pages", _I64), ("page_tokens", ctypes.c_int32)]
+
+    def __init__(self, refs: torch.Tensor, page_tokens: int):
+        _need(refs, "refs", torch.int32)
+        if refs.dim() != 1:
+            raise ValueError(f"refs must have shape (pages,), got {tuple(refs.shape)}")
+        self.refs, self.pages, self.page_tokens = refs, refs.shape[0], int(page_tokens)
+        self.struct = KVPool._Struct(refs.data_ptr(), self.pages, self.page_tokens)
+        self.address = ctypes.addressof(self.struct)
+
+    @classmethod
+    def empty(cls, pages: int, page_tokens: int, device) -> "KVPool":
+        """A pool of its own, all pages free."""
+        return cls(torch.zeros(pages, dtype=torch.int32, device=device), page_tokens)
+
+
+class KVCaches:
+    """The caches of a model's blocks, all of one shape, for bl_kv_copy."""
+
+    def __init__(self, caches):
+        self.caches = list(caches)
+        self.structs = (KVCache._Struct * max(len(self.caches), 1))(*[c.struct for c in self.caches])
+        self.address = ctypes.addressof(self.structs)
+
+    def __len__(self) -> int:
+        return len(self.caches)
+
+
+def _table(t: torch.Tensor, name: str) -> tuple[int, int, int]:
+    """Address, sequences and entries per sequence of an int32 page table."""
+    if t.dtype is not torch.int32 or not t.is_contiguous() or not t.is_cuda:
+        _need(t, name, torch.int32)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have shape (seqs, stride), got {tuple(t.shape)}")
+    return t.data_ptr(), t.shape[0], t.shape[1]
+
+
+def bl_kv_grow(pool: KVPool, batch: KVBatch, copies: torch.Tensor | None = None,
+               shortage: torch.Tensor | None = None) -> None:
+    """Gives pages to the entries of the batch's page table in which its new tokens stand and that have none.
+    ``copies`` (int32 [seqs][3], optional) takes what bl_kv_copy has to copy where a sequence would go on writing in a
+    page that others hold too; ``shortage`` (int32 [1], optional) grows by the number of requests for which no page
+    was free."""
+    _check("bl_kv_grow", _lib.bl_kv_grow(
+        pool.address, batch.address, _dense(copies, "copies", torch.int32, (batch.page_table.shape[0], 3)),
+        _dense(shortage, "shortage", torch.int32, (1,)), _stream(pool.refs.device)))
+
+
+def bl_kv_fork(pool: KVPool, page_table: torch.Tensor, length: torch.Tensor, parent: torch.Tensor,
+               keep_parents: bool = False, table: torch.Tensor | None = None, out_length: torch.Tensor | None = None,
+               copies: torch.Tensor | None = None, shortage: torch.Tensor | None = None):
+    """Children of the sequences in ``page_table`` (int32 [seqs][stride]) that hold ``length`` [seqs] tokens: child
+    ``c`` continues sequence ``parent[c]``.  Returns (table [children][stride], out_length [children], copies
+    [children][3]); bl_kv_copy makes the copies.  Without ``keep_parents`` the parents are given up."""
+    tp, seqs, stride = _table(page_table, "page_table")
+    children = parent.shape[0]
+    dev = page_table.device
+    if table is None:
+        table = torch.empty((children, stride), dtype=torch.int32, device=dev)
+    if out_length is None:
+        out_length = torch.empty(children, dtype=torch.int32, device=dev)
+    if copies is None:
+        copies = torch.empty((children, 3), dtype=torch.int32, device=dev)
+    _check("bl_kv_fork", _lib.bl_kv_fork(
+        pool.address, tp, stride, _dense(length, "length", torch.int32, (seqs,)), seqs,
+        _dense(parent, "parent", torch.int32, (children,)), children, int(keep_parents),
+        _dense(table, "table", torch.int32, (children, stride)), _dense(out_length, "out_length", torch.int32, (children,)),
+        _dense(copies, "copies", torch.int32, (children, 3)), _dense(shortage, "shortage", torch.int32, (1,)), _stream(dev)))
+    return table, out_length, copies
+
+
+def bl_kv_free(pool: KVPool, page_table: torch.Tensor, keep: torch.Tensor | None = None) -> None:
+    """Row s of ``page_table`` keeps the pages of its first ``keep[s]`` tokens (int32; none without ``keep``) and gives
+    the others back."""
+    tp, seqs, stride = _table(page_table, "page_table")
+    _check("bl_kv_free", _lib.bl_kv_free(pool.address, tp, stride, seqs, _dense(keep, "keep", torch.int32, (seqs,)),
+                                         _stream(page_table.device)))
+
+
+def bl_kv_compact_workspace_bytes(pool: KVPool, moves: int) -> int:
+    return int(_lib.bl_kv_compact_workspace_bytes(pool.address, moves))
+
+
+def bl_kv_compact(pool: KVPool, page_table: torch.Tensor, moves: int, copies: torch.Tensor | None = None,
+                  moved: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Moves up to ``moves`` used pages, the highest first, to the lowest free ones and renames them in
+    ``page_table``, which holds every row that has pages of the pool.  Returns (copies [moves][3], moved [1]) for
+    bl_kv_copy."""
+    tp, seqs, stride = _table(page_table, "page_table")
+    dev = page_table.device
+    if copies is None:
+        copies = torch.empty((moves, 3), dtype=torch.int32, device=dev)
+    if moved is None:
+        moved = torch.empty(1, dtype=torch.int32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(max(bl_kv_compact_workspace_bytes(pool, moves), 16), dtype=torch.uint8, device=dev)
+    _check("bl_kv_compact", _lib.bl_kv_compact(
+        pool.address, tp, stride, seqs, moves, _dense(copies, "copies", torch.int32, (moves, 3)),
+        _dense(moved, "moved", torch.int32, (1,)), workspace.data_ptr(), _bytes(workspace), _stream(dev)))
+    return copies, moved
+
+
+def bl_kv_copy(caches: KVCaches | KVCache, copies: torch.Tensor, count: torch.Tensor | None = None) -> None:
+    """Copies pages inside each cache: rows (source, target, tokens) of ``copies`` (int32 [n][3]), the first
+    ``count`` (int32 [1] on the device) of them if it is given."""
+    n = copies.shape[0]
+    many = len(caches) if isinstance(caches, KVCaches) else 1
+    _check("bl_kv_copy", _lib.bl_kv_copy(caches.address, many, _dense(copies, "copies", torch.int32, (n, 3)), n,
+                                         _dense(count, "count", torch.int32, (1,)), _stream(copies.device)))
+
+
+_LOGIT_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _logits(t: torch.Tensor, name: str) -> tuple[int, int, int]:
+    """Address, type and row stride of logits [m][n] whose last axis is adjacent."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype not in _LOGIT_TYPES:
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have shape (m, n), got {tuple(t.shape)}")
+    m, n = t.shape
+    row, one = t.stride()
+    if one != 1 and n > 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    return t.data_ptr(), _LOGIT_TYPES[t.dtype], max(n, 1) if m <= 1 else row
+
+
+def bl_logprobs_workspace_bytes(m: int, n: int, dtype: torch.dtype = torch.bfloat16, top: int = 0) -> int:
+    return int(_lib.bl_logprobs_workspace_bytes(m, n, _LOGIT_TYPES[dtype], top))
+
+
+def bl_logprobs(logits: torch.Tensor, target: torch.Tensor | None = None, scale: float = 1.0, top: int = 0,
+                logprob: torch.Tensor | None = None, lse: torch.Tensor | None = None, entropy: torch.Tensor | None = None,
+                top_id: torch.Tensor | None = None, top_logprob: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None):
+    """Of logits [m][n] (bf16 or fp32) times ``scale``: (logprob of the int32 tokens ``target`` [m], None without
+    them; lse; entropy; top_id, top_logprob [m][top] of the most likely tokens, None without ``top``), fp32."""
+    xp, kind, stride = _logits(logits, "logits")
+    m, n = logits.shape
+    dev = logits.device
+    if target is None:
+        logprob = None
+    elif logprob is None:
+        logprob = torch.empty(m, dtype=torch.float32, device=dev)
+    if lse is None:
+        lse = torch.empty(m, dtype=torch.float32, device=dev)
+    if entropy is None:
+        entropy = torch.empty(m, dtype=torch.float32, device=dev)
+    if not top:
+        top_id = top_logprob = None
+    else:
+        if top_id is None:
+            top_id = torch.empty((m, top), dtype=torch.int32, device=dev)
+        if top_logprob is None:
+            top_logprob = torch.empty((m, top), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(max(bl_logprobs_workspace_bytes(m, n, logits.dtype, top), 16), dtype=torch.uint8, device=dev)
+    _check("bl_logprobs", _lib.bl_logprobs(
+        xp, kind, m, n, stride, scale, _dense(target, "target", torch.int32, (m,)), top,
+        _dense(logprob, "logprob", torch.float32, (m,)), _dense(lse, "lse", torch.float32, (m,)),
+        _dense(entropy, "entropy", torch.float32, (m,)), _dense(top_id, "top_id", torch.int32, (m, top)),
+        _dense(top_logprob, "top_logprob", torch.float32, (m, top)), workspace.data_ptr(), _bytes(workspace), _stream(dev)))
+    return logprob, lse, entropy, top_id, top_logprob
+
+
+def bl_logprobs_backward(logits: torch.Tensor, target: torch.Tensor | None, lse: torch.Tensor,
+                         entropy: torch.Tensor | None, dlogprob: torch.Tensor | None,
+                         dentropy: torch.Tensor | None = None, dlse: torch.Tensor | None = None, scale: float = 1.0,
+                         dlogits: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of the logits (their type) for the fp32 gradients [m] of logprob, entropy and lse (None: zeros), with
+    the lse and entropy that bl_logprobs gave.  ``dlogits`` may be ``logits``."""
+    xp, kind, stride = _logits(logits, "logits")
+    m, n = logits.shape
+    if dlogits is None:
+        dlogits = torch.empty((m, n), dtype=logits.dtype, device=logits.device)
+    dp, d_kind, d_stride = _logits(dlogits, "dlogits")
+    if d_kind != kind or dlogits.shape != logits.shape:
+        raise ValueError(f"dlogits must be {logits.dtype} of shape {(m, n)}, got {dlogits.dtype} {tuple(dlogits.shape)}")
+    if m > 1 and dlogits.stride(0) < n:
+        raise ValueError("rows of dlogits must not overlap")
+    f32 = lambda t, name: _dense(t, name, torch.float32, (m,))  # noqa: E731
+    _check("bl_logprobs_backward", _lib.bl_logprobs_backward(
+        xp, kind, m, n, stride, scale, _dense(target, "target", torch.int32, (m,)), f32(lse, "lse"), f32(entropy, "entropy"),
+        f32(dlogprob, "dlogprob"), f32(dentropy, "dentropy"), f32(dlse, "dlse"), dp, d_stride, _stream(logits.device)))
+    return dlogits

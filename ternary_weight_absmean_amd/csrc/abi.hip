@@ -310,22 +310,34 @@ bool strides_ok(int64_t token, int64_t head) { return token % 8 == 0 && head % 8
 // The kernels count tokens, positions and heads in 32 bits.
 constexpr int64_t kMaxPositions = (int64_t)1 << 29;
 
+bool page_tokens_ok(int p) { return p == 16 || p == 32 || p == 64 || p == 128 || p == 256; }
+
+bl_status check_cache(const bl_kv_cache* c) {
+  if (c->heads < 1 || c->heads > 65536 || !page_tokens_ok(c->page_tokens) || c->dim < 16 || c->dim > BL_MAX_HEAD_DIM ||
+      c->dim % 16 != 0 || c->pages < 1 || c->pages > 0x7FFFFFFF ||
+      !product_ok(c->pages, (int64_t)c->heads * c->page_tokens * c->dim))
+    return BL_ERR_SHAPE;
+  return BL_OK;
+}
+
+bl_status check_cache_pointers(const bl_kv_cache* c) {
+  if (!c->k || !c->v || !c->k_absmax || !c->v_absmax) return BL_ERR_NULL;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_absmax, 4) || !aligned(c->v_absmax, 4)) return BL_ERR_ALIGN;
+  return BL_OK;
+}
+
 bl_status check_kv(const bl_kv_cache* c, const bl_kv_batch* b) {
   if (!c || !b) return BL_ERR_NULL;
   const int p = c->page_tokens;
-  if (c->heads < 1 || c->heads > 65536 || (p != 16 && p != 32 && p != 64 && p != 128 && p != 256) || c->dim < 16 ||
-      c->dim > BL_MAX_HEAD_DIM || c->dim % 16 != 0 || c->pages < 1 || c->pages > 0x7FFFFFFF ||
-      !product_ok(c->pages, (int64_t)c->heads * p * c->dim))
-    return BL_ERR_SHAPE;
+  if (bl_status st = check_cache(c)) return st;
   if (b->seqs < 0 || b->seqs > 65535 || b->tokens < 0 || b->tokens > kMaxPositions || b->max_new < 0 ||
       b->max_new > b->tokens || b->max_len < b->max_new || b->max_len > kMaxPositions || b->table_stride < 0 ||
       b->table_stride > 0x7FFFFFFF || b->max_len > b->table_stride * p)
     return BL_ERR_SHAPE;
   if (b->seqs == 0 || b->tokens == 0 || b->max_new == 0) return BL_OK;
-  if (!c->k || !c->v || !c->k_absmax || !c->v_absmax || !b->page_table || !b->start || !b->offsets) return BL_ERR_NULL;
-  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_absmax, 4) || !aligned(c->v_absmax, 4) ||
-      !aligned(b->page_table, 4) || !aligned(b->start, 4) || !aligned(b->offsets, 4))
-    return BL_ERR_ALIGN;
+  if (!b->page_table || !b->start || !b->offsets) return BL_ERR_NULL;
+  if (bl_status st = check_cache_pointers(c)) return st;
+  if (!aligned(b->page_table, 4) || !aligned(b->start, 4) || !aligned(b->offsets, 4)) return BL_ERR_ALIGN;
   return BL_OK;
 }
 
@@ -433,6 +445,149 @@ bl_status bl_attention(const bl_kv_cache* cache, const bl_kv_batch* batch, const
   return from_hip(bl::launch_attention(kv, step_of(batch), batch->seqs, batch->tokens, batch->max_new, batch->max_len, q,
                                        q_token_stride, q_head_stride, (int)q_heads, scale, window, sinks, out, lse,
                                        workspace, (hipStream_t)stream));
+}
+
+namespace {
+
+// A pool, and a table of `seqs` rows that goes with it.
+bl_status check_pool(const bl_kv_pool* pool, int64_t seqs, int64_t stride) {
+  if (!pool) return BL_ERR_NULL;
+  if (pool->pages < 1 || pool->pages > BL_MAX_POOL_PAGES || !page_tokens_ok(pool->page_tokens) || seqs < 0 || seqs > 65535 ||
+      stride < 0 || stride > kMaxPositions / pool->page_tokens)
+    return BL_ERR_SHAPE;
+  return BL_OK;
+}
+
+}  // namespace
+
+bl_status bl_kv_grow(const bl_kv_pool* pool, const bl_kv_batch* batch, int32_t* copies, int32_t* shortage, void* stream) {
+  if (!pool || !batch) return BL_ERR_NULL;
+  if (bl_status st = check_pool(pool, batch->seqs, batch->table_stride)) return st;
+  if (batch->tokens < 0 || batch->tokens > kMaxPositions || batch->max_new < 0 || batch->max_new > batch->tokens ||
+      batch->max_len < batch->max_new || batch->max_len > batch->table_stride * pool->page_tokens ||
+      batch->seqs * ((batch->max_new + pool->page_tokens - 2) / pool->page_tokens + 1) > bl::kMaxGrowItems)
+    return BL_ERR_SHAPE;
+  if (nothing_new(batch)) return BL_OK;  // empty tensors may carry NULL pointers
+  if (!pool->refs || !batch->page_table || !batch->start || !batch->offsets) return BL_ERR_NULL;
+  if (!aligned(pool->refs, 16) || !aligned(batch->page_table, 4) || !aligned(batch->start, 4) ||
+      !aligned(batch->offsets, 4) || !aligned(copies, 4) || !aligned(shortage, 4))
+    return BL_ERR_ALIGN;
+  return from_hip(bl::launch_kv_grow(pool->refs, pool->pages, pool->page_tokens, step_of(batch), batch->seqs, batch->max_new,
+                                     const_cast<int32_t*>(batch->page_table), copies, shortage, (hipStream_t)stream));
+}
+
+bl_status bl_kv_fork(const bl_kv_pool* pool, const int32_t* table, int64_t table_stride, const int32_t* length,
+                     int64_t seqs, const int32_t* parent, int64_t children, int keep_parents, int32_t* table_out,
+                     int32_t* length_out, int32_t* copies, int32_t* shortage, void* stream) {
+  if (bl_status st = check_pool(pool, seqs, table_stride)) return st;
+  if (seqs > BL_MAX_FORK_SEQS || children < 0 || children > BL_MAX_FORK_SEQS || (table && table_out == table)) return BL_ERR_SHAPE;
+  if ((children == 0 && (keep_parents || seqs == 0)) || (seqs > 0 && table_stride == 0 && children == 0)) return BL_OK;
+  if (!pool->refs || (seqs > 0 && (!length || (table_stride > 0 && !table))) ||
+      (children > 0 && (!parent || !length_out || !copies || (table_stride > 0 && !table_out))))
+    return BL_ERR_NULL;
+  if (!aligned(pool->refs, 16) || !aligned(table, 4) || !aligned(length, 4) || !aligned(parent, 4) ||
+      !aligned(table_out, 4) || !aligned(length_out, 4) || !aligned(copies, 4) || !aligned(shortage, 4))
+    return BL_ERR_ALIGN;
+  return from_hip(bl::launch_kv_fork(pool->refs, pool->pages, pool->page_tokens, table, table_stride, length, seqs, parent,
+                                     children, keep_parents != 0, table_out, length_out, copies, shortage,
+                                     (hipStream_t)stream));
+}
+
+bl_status bl_kv_free(const bl_kv_pool* pool, int32_t* table, int64_t table_stride, int64_t seqs, const int32_t* keep,
+                     void* stream) {
+  if (bl_status st = check_pool(pool, seqs, table_stride)) return st;
+  if (seqs == 0 || table_stride == 0) return BL_OK;  // empty tensors may carry NULL pointers
+  if (!pool->refs || !table) return BL_ERR_NULL;
+  if (!aligned(pool->refs, 16) || !aligned(table, 4) || !aligned(keep, 4)) return BL_ERR_ALIGN;
+  return from_hip(bl::launch_kv_free(pool->refs, pool->pages, pool->page_tokens, table, table_stride, seqs, keep,
+                                     (hipStream_t)stream));
+}
+
+size_t bl_kv_compact_workspace_bytes(const bl_kv_pool* pool, int64_t moves) {
+  if (check_pool(pool, 0, 0) != BL_OK || moves < 0 || moves > pool->pages) return 0;
+  return bl::kv_compact_workspace_bytes(pool->pages, moves);
+}
+
+bl_status bl_kv_compact(const bl_kv_pool* pool, int32_t* table, int64_t table_stride, int64_t seqs, int64_t moves,
+                        int32_t* copies, int32_t* moved, void* workspace, size_t workspace_bytes, void* stream) {
+  if (bl_status st = check_pool(pool, seqs, table_stride)) return st;
+  if (moves < 0 || moves > pool->pages) return BL_ERR_SHAPE;
+  if (!pool->refs || !moved || !workspace || (moves > 0 && !copies) || (seqs * table_stride > 0 && !table)) return BL_ERR_NULL;
+  if (!aligned(pool->refs, 16) || !aligned(table, 4) || !aligned(copies, 4) || !aligned(moved, 4) || !aligned(workspace, 16))
+    return BL_ERR_ALIGN;
+  if (workspace_bytes < bl::kv_compact_workspace_bytes(pool->pages, moves)) return BL_ERR_WORKSPACE;
+  return from_hip(bl::launch_kv_compact(pool->refs, pool->pages, pool->page_tokens, table, table_stride, seqs, moves, copies,
+                                        moved, workspace, (hipStream_t)stream));
+}
+
+bl_status bl_kv_copy(const bl_kv_cache* caches, int64_t count, const int32_t* copies, int64_t n, const int32_t* valid,
+                     void* stream) {
+  if (count < 0 || count > bl::kMaxCaches || n < 0 || n > BL_MAX_POOL_PAGES) return BL_ERR_SHAPE;
+  if (count > 0 && !caches) return BL_ERR_NULL;
+  bl::KvView views[bl::kMaxCaches];
+  for (int64_t i = 0; i < count; ++i) {
+    if (bl_status st = check_cache(caches + i)) return st;
+    if (caches[i].pages != caches[0].pages || caches[i].heads != caches[0].heads ||
+        caches[i].page_tokens != caches[0].page_tokens || caches[i].dim != caches[0].dim)
+      return BL_ERR_SHAPE;
+    views[i] = view(caches + i);
+  }
+  if (count == 0 || n == 0) return BL_OK;  // empty tensors may carry NULL pointers
+  for (int64_t i = 0; i < count; ++i)
+    if (bl_status st = check_cache_pointers(caches + i)) return st;
+  if (!copies) return BL_ERR_NULL;
+  if (!aligned(copies, 4) || !aligned(valid, 4)) return BL_ERR_ALIGN;
+  return from_hip(bl::launch_kv_copy(views, count, copies, n, valid, (hipStream_t)stream));
+}
+
+namespace {
+
+bl_status check_logits(int type, int64_t m, int64_t n, int64_t stride, float scale) {
+  if ((type != BL_BF16 && type != BL_FP32) || m < 0 || m > BL_MAX_M || n < 1 || n > BL_MAX_VOCABULARY || stride < n ||
+      !product_ok(m, stride) || !(scale > 0.0f && scale < INFINITY))
+    return BL_ERR_SHAPE;
+  return BL_OK;
+}
+
+}  // namespace
+
+size_t bl_logprobs_workspace_bytes(int64_t m, int64_t n, int type, int64_t top) {
+  if (check_logits(type, m, n, n, 1.0f) != BL_OK || m == 0 || top < 0 || top > BL_MAX_TOP) return 0;
+  return bl::logprobs_workspace_bytes(m, n, type == BL_BF16, top);
+}
+
+bl_status bl_logprobs(const void* x, int type, int64_t m, int64_t n, int64_t row_stride, float scale,
+                      const int32_t* target, int64_t top, float* logprob, float* lse, float* entropy, int32_t* top_id,
+                      float* top_logprob, void* workspace, size_t workspace_bytes, void* stream) {
+  if (bl_status st = check_logits(type, m, n, row_stride, scale)) return st;
+  if (top < 0 || top > BL_MAX_TOP) return BL_ERR_SHAPE;
+  if (m == 0) return BL_OK;  // empty tensors may carry NULL pointers
+  if (!x || (logprob && !target) || (top > 0 && (!top_id || !top_logprob)) || (!logprob && !lse && !entropy && top == 0))
+    return BL_ERR_NULL;
+  if (!aligned(x, type == BL_BF16 ? 2 : 4) || !aligned(target, 4) || !aligned(logprob, 4) || !aligned(lse, 4) ||
+      !aligned(entropy, 4) || !aligned(top_id, 4) || !aligned(top_logprob, 4) || !aligned(workspace, 16))
+    return BL_ERR_ALIGN;
+  const size_t need = bl::logprobs_workspace_bytes(m, n, type == BL_BF16, top);
+  if (need > 0 && !workspace) return BL_ERR_NULL;
+  if (need > workspace_bytes) return BL_ERR_WORKSPACE;
+  return from_hip(bl::launch_logprobs(x, type == BL_BF16, m, n, row_stride, scale, target, top, logprob, lse, entropy, top_id,
+                                      top_logprob, workspace, (hipStream_t)stream));
+}
+
+bl_status bl_logprobs_backward(const void* x, int type, int64_t m, int64_t n, int64_t row_stride, float scale,
+                               const int32_t* target, const float* lse, const float* entropy, const float* dlogprob,
+                               const float* dentropy, const float* dlse, void* dx, int64_t dx_stride, void* stream) {
+  if (bl_status st = check_logits(type, m, n, row_stride, scale)) return st;
+  if (dx_stride < n || !product_ok(m, dx_stride) || (x && dx == x && dx_stride != row_stride && m > 1)) return BL_ERR_SHAPE;
+  if (m == 0) return BL_OK;  // empty tensors may carry NULL pointers
+  if (!x || !lse || !dx || (!dlogprob && !dentropy && !dlse) || (dlogprob && !target) || (dentropy && !entropy))
+    return BL_ERR_NULL;
+  const uintptr_t size = type == BL_BF16 ? 2 : 4;
+  if (!aligned(x, size) || !aligned(dx, size) || !aligned(target, 4) || !aligned(lse, 4) || !aligned(entropy, 4) ||
+      !aligned(dlogprob, 4) || !aligned(dentropy, 4) || !aligned(dlse, 4))
+    return BL_ERR_ALIGN;
+  return from_hip(bl::launch_logprobs_backward(x, type == BL_BF16, m, n, row_stride, scale, target, lse, entropy, dlogprob,
+                                               dentropy, dlse, dx, dx_stride, (hipStream_t)stream));
 }
 
 const char* bl_status_string(bl_status s) {

@@ -134,6 +134,35 @@ hipError_t launch_kv_append(const KvView& kv, const KvStep& st, int64_t seqs, in
 hipError_t launch_kv_read(const KvView& kv, const KvStep& st, int64_t seqs, int64_t max_new, uint16_t* k, uint16_t* v,
                           hipStream_t s);
 
+// Pages of the cache: reference counts, page tables, copies (src, dst, tokens).
+constexpr int kMaxForkSeqs = 8192;                        // parents, and children, of a fork
+constexpr int64_t kMaxGrowItems = (int64_t)1 << 24;       // pages that the sequences of a step may enter
+constexpr int kCopyCaches = 32;                           // caches per launch of the copy
+constexpr int kMaxCaches = 1024;                          // per call of it
+hipError_t launch_kv_grow(int32_t* refs, int64_t pages, int page_tokens, const KvStep& st, int64_t seqs, int64_t max_new,
+                          int32_t* table, int32_t* copies, int32_t* shortage, hipStream_t s);
+hipError_t launch_kv_fork(int32_t* refs, int64_t pages, int page_tokens, const int32_t* table, int64_t stride,
+                          const int32_t* length, int64_t seqs, const int32_t* parent, int64_t children, bool keep_parents,
+                          int32_t* table_out, int32_t* length_out, int32_t* copies, int32_t* shortage, hipStream_t s);
+hipError_t launch_kv_free(int32_t* refs, int64_t pages, int page_tokens, int32_t* table, int64_t stride, int64_t seqs,
+                          const int32_t* keep, hipStream_t s);
+size_t kv_compact_workspace_bytes(int64_t pages, int64_t moves);
+hipError_t launch_kv_compact(int32_t* refs, int64_t pages, int page_tokens, int32_t* table, int64_t stride, int64_t seqs,
+                             int64_t moves, int32_t* copies, int32_t* moved, void* workspace, hipStream_t s);
+hipError_t launch_kv_copy(const KvView* caches, int64_t count, const int32_t* copies, int64_t n, const int32_t* valid,
+                          hipStream_t s);
+
+// Log probabilities, entropy and alternatives of rows of logits; the gradient.
+constexpr int kMaxTop = 64;
+constexpr int kMaxLogChunks = 64;  // parts of a row that a workgroup joins, one per lane
+size_t logprobs_workspace_bytes(int64_t m, int64_t n, bool bf16, int64_t top);
+hipError_t launch_logprobs(const void* x, bool bf16, int64_t m, int64_t n, int64_t stride, float scale,
+                           const int32_t* target, int64_t top, float* logprob, float* lse, float* entropy, int32_t* top_id,
+                           float* top_logprob, void* workspace, hipStream_t s);
+hipError_t launch_logprobs_backward(const void* x, bool bf16, int64_t m, int64_t n, int64_t stride, float scale,
+                                    const int32_t* target, const float* lse, const float* entropy, const float* g,
+                                    const float* gh, const float* gz, void* dx, int64_t dx_stride, hipStream_t s);
+
 size_t attention_workspace_bytes(const KvView& kv, int64_t seqs, int64_t tokens, int64_t max_new, int64_t max_len,
                                  int64_t q_heads);
 hipError_t launch_attention(const KvView& kv, const KvStep& st, int64_t seqs, int64_t tokens, int64_t max_new,

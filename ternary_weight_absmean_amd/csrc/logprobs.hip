@@ -1,0 +1,500 @@
+// Log probabilities of given tokens, entropy and the most likely alternatives
+// (bl_logprobs), and their gradient (bl_logprobs_backward).
+//
+// With c = scale * log2 e, M = max x and d_j = (x_j - M) c:
+//   S = sum 2^d_j,  W = sum 2^d_j d_j,
+//   lse = scale M + ln S,  logprob_j = scale (x_j - M) - ln S,
+//   entropy = (log2 S - W / S) ln 2.
+// Differences are taken before the scale, so that rows of the type's lowest
+// value do not overflow.  All sums are fp32.
+//
+// A row is cut into chunks that one workgroup each holds in registers: one
+// reading of the logits gives the chunk's maximum, then (from the registers) S, W and
+// the candidates for the alternatives.  A second kernel joins the chunks of a
+// row.  HBM-bound.
+//
+// Alternatives.  Wave w's r-th largest of its lanes' maxima, r = ceil(top /
+// waves), has r elements of that wave at or above it, so at least top elements
+// of the chunk are at or above the smallest of these over the waves: those are
+// collected in LDS (a few times top of them, as a rule) and ranked by counting.
+// Where they are too many (equal logits, logits in ascending order) the top-th
+// largest is found by bisection over the registers first.
+#include "device_util.h"
+#include "internal.h"
+
+namespace bl {
+namespace {
+
+typedef unsigned v4u __attribute__((ext_vector_type(4)));
+
+constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / 64;
+constexpr int kCandidates = 1024;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLowest = -0x1.fffffep127f;
+
+struct LogArgs {
+  const char* x;
+  int64_t stride;  // bytes
+  int n, chunks, top;
+  float scale, c;  // c = scale * log2 e
+  const int32_t* target;
+  float *logprob, *lse, *entropy;
+  int32_t* top_id;
+  float* top_logprob;
+  float* stats;  // [row][chunk][4]: max, S, W, candidates
+  uint2* best;   // [row][chunk][top]: value, index
+};
+
+// Elements of a row by 16-byte pieces: up to 16 / size - 1 before the first
+// aligned address, whole pieces, the rest.
+template <bool kBf16>
+struct Pieces {
+  static constexpr int kSize = kBf16 ? 2 : 4, kPer = 16 / kSize;
+  const char* row;
+  int head, vecs, tail;
+  __device__ Pieces(const char* x, int64_t stride, int64_t r, int n) : row(x + r * stride) {
+    head = min((int)(-(intptr_t)row & 15) / kSize, n);
+    vecs = (n - head) / kPer;
+    tail = n - head - vecs * kPer;
+  }
+  __device__ const v4u* vec(int i) const { return reinterpret_cast<const v4u*>(row + head * kSize) + i; }
+  __device__ float at(int j) const {
+    if (kBf16) return __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(row)[j] << 16);
+    return reinterpret_cast<const float*>(row)[j];
+  }
+  // the t-th element outside whole pieces
+  __device__ int edge(int t) const { return t < head ? t : vecs * kPer + t; }
+  __device__ int edges() const { return head + tail; }
+};
+
+template <bool kBf16>
+__device__ __forceinline__ float element(const v4u& v, int j) {
+  if (kBf16) return __uint_as_float(j & 1 ? v[j >> 1] & 0xFFFF0000u : v[j >> 1] << 16);
+  return __uint_as_float(v[j]);
+}
+
+// Integers that order like the values, -0 like +0.
+__device__ __forceinline__ int order_of(float f) {
+  const int b = __float_as_int(f + 0.0f);
+  return b ^ (b >> 31 & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float value_of(int order) { return __int_as_float(order ^ (order >> 31 & 0x7FFFFFFF)); }
+
+// Larger values first, then lower indices: one number for both, no two alike.
+__device__ __forceinline__ uint64_t place_of(float value, uint32_t index) {
+  return (uint64_t)((uint32_t)order_of(value) ^ 0x80000000u) << 32 | (0xFFFFFFFFu - index);
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+
+// The r-th largest of the lanes' values (as order_of), INT_MIN if there is none.
+__device__ __forceinline__ int wave_rth(int v, int r) {
+  int top = wave_reduce<true>(v);
+  for (int i = 1; i < r; ++i) {
+    const uint64_t at = __ballot(v == top);
+    if ((int)(threadIdx.x & 63) == __ffsll((unsigned long long)at) - 1) v = INT_MIN;
+    top = wave_reduce<true>(v);
+  }
+  return top;
+}
+
+struct Final {
+  float top, scale, log_s, entropy, lse;
+  // max, S and W of a whole row; S is 0 where nothing is possible
+  __device__ Final(const LogArgs& a, float most, float s, float w) : top(most), scale(a.scale), log_s(__log2f(s) * kLn2) {
+    entropy = s == 0.0f ? 0.0f : __builtin_fmaf(w / s, -kLn2, log_s);
+    lse = s == 0.0f ? -INFINITY : __builtin_fmaf(top, scale, log_s);
+  }
+  __device__ float logprob(float x) const {
+    return x == -INFINITY && log_s == log_s ? -INFINITY : __builtin_fmaf(x - top, scale, -log_s);
+  }
+};
+
+template <bool kBf16>
+__device__ __forceinline__ void store_row(const LogArgs& a, int64_t row, const Final& f) {
+  if (a.lse) a.lse[row] = f.lse;
+  if (a.entropy) a.entropy[row] = f.entropy;
+  if (a.logprob) {
+    const int t = a.target[row];
+    float v = 0.0f;
+    if ((uint32_t)t < (uint32_t)a.n) v = f.logprob(Pieces<kBf16>(a.x, a.stride, row, a.n).at(t));
+    a.logprob[row] = v;
+  }
+}
+
+// Puts the `top` best of `count` candidates into out(rank, place), in order.
+template <int kBlock, typename Out>
+__device__ __forceinline__ void rank_candidates(const uint64_t* place, int count, int top, Out out) {
+  for (int i = threadIdx.x; i < count; i += kBlock) {
+    const uint64_t mine = place[i];
+    int rank = 0;
+    for (int j = 0; j < count; ++j) rank += place[j] > mine;
+    if (rank < top) out(rank, mine);
+  }
+}
+
+template <bool kBf16, int E, bool kTop>
+__global__ __launch_bounds__(kThreads) void k_logprobs(LogArgs a) {
+  constexpr int kPer = Pieces<kBf16>::kPer;
+  __shared__ float wave_top[kWaves], wave_s[kWaves], wave_w[kWaves];
+  __shared__ int wave_limit[kWaves], counter[2];
+  __shared__ uint64_t place[kTop ? kCandidates : 1];
+  const int64_t row = blockIdx.x / a.chunks;
+  const int chunk = (int)(blockIdx.x - row * a.chunks);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const Pieces<kBf16> p(a.x, a.stride, row, a.n);
+  const int per = (p.vecs + a.chunks - 1) / a.chunks, v0 = min(chunk * per, p.vecs), v1 = min(v0 + per, p.vecs);
+  if (kTop && tid == 0) counter[0] = 0;
+
+  const uint32_t none = kBf16 ? 0xFF80FF80u : 0xFF800000u;  // -infinity, which counts for nothing
+  v4u data[E];
+  if (v0 < v1) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) data[i] = *p.vec(min(v0 + i * kThreads + tid, v1 - 1));
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    if (v0 + i * kThreads + tid >= v1) data[i] = (v4u){none, none, none, none};
+  float edge = -INFINITY;
+  if (chunk == 0 && tid < p.edges()) edge = p.at(p.edge(tid));
+
+  float most[E], top = edge == edge ? edge : -INFINITY;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    most[i] = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) most[i] = fmaxf(most[i], element<kBf16>(data[i], j));
+    top = fmaxf(top, most[i]);
+  }
+  const int key = order_of(top);
+  const int wave_key = wave_reduce<true>(key);
+  if (lane == 0) wave_top[wave] = value_of(wave_key);
+  const int full = max(min((v1 - v0) / 64, kWaves), 1);  // waves with an element in every lane
+  if (kTop) {
+    const int limit = wave_rth(key, (a.top + full - 1) / full);
+    if (lane == 0) wave_limit[wave] = limit;
+  }
+  __syncthreads();
+  top = wave_top[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) top = fmaxf(top, wave_top[w]);
+  float limit = INFINITY;
+  if (kTop) {
+    int least = wave_limit[0];
+    for (int w = 1; w < full; ++w) least = min(least, wave_limit[w]);
+    limit = fmaxf(value_of(max(least, order_of(-INFINITY))), kLowest);  // -infinity is no candidate
+  }
+
+  const float most_finite = top == -INFINITY ? 0.0f : top;
+  float s = 0.0f, w = 0.0f;
+  auto add = [&](float x) {
+    const float d = (x - most_finite) * a.c, e = __builtin_amdgcn_exp2f(d);
+    s += e;
+    w = __builtin_fmaf(e, fmaxf(d, -300.0f), w);  // 0 * -infinity is 0 here
+  };
+  // this thread's elements, each with its index
+  auto each = [&](auto f) {
+    if (edge > -INFINITY) f(edge, (uint32_t)p.edge(tid));
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const uint32_t first = (uint32_t)(p.head + (v0 + i * kThreads + tid) * kPer);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) f(element<kBf16>(data[i], j), first + j);
+    }
+  };
+  auto collect = [&](float x, uint32_t index) {
+    const int at = atomicAdd(&counter[0], 1);
+    if (at < kCandidates) place[at] = place_of(x, index);
+  };
+  add(edge);
+  if (kTop && edge >= limit) collect(edge, (uint32_t)p.edge(tid));
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) add(element<kBf16>(data[i], j));
+    if (kTop && most[i] >= limit) {
+      const uint32_t first = (uint32_t)(p.head + (v0 + i * kThreads + tid) * kPer);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (element<kBf16>(data[i], j) >= limit) collect(element<kBf16>(data[i], j), first + j);
+    }
+  }
+  s = wave_sum(s);
+  w = wave_sum(w);
+  if (lane == 0) {
+    wave_s[wave] = s;
+    wave_w[wave] = w;
+  }
+  __syncthreads();
+  int count = kTop ? counter[0] : 0;
+  if (kTop && count > kCandidates) {
+    // the largest place that `top` elements reach, bit by bit
+    uint64_t reach = 0;
+    for (int bit = 63; bit >= 0; --bit) {
+      const uint64_t tried = reach | (uint64_t)1 << bit;
+      int here = 0;
+      each([&](float x, uint32_t index) { here += x > -INFINITY && place_of(x, index) >= tried; });
+      here = wave_reduce<false>(here);
+      __syncthreads();
+      if (lane == 0) wave_limit[wave] = here;
+      __syncthreads();
+      int all = 0;
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) all += wave_limit[i];
+      if (all >= a.top) reach = tried;
+    }
+    if (tid == 0) counter[0] = 0;
+    __syncthreads();
+    each([&](float x, uint32_t index) {
+      if (x > -INFINITY && place_of(x, index) >= reach) collect(x, index);
+    });
+    __syncthreads();
+    count = counter[0];
+  }
+  s = w = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    s += wave_s[i];
+    w += wave_w[i];
+  }
+  if (a.chunks == 1) {
+    const Final f(a, top, s, w);
+    if (tid == 0) store_row<kBf16>(a, row, f);
+    if (kTop) {
+      int32_t* ids = a.top_id + row * a.top;
+      float* values = a.top_logprob + row * a.top;
+      rank_candidates<kThreads>(place, count, a.top, [&](int rank, uint64_t q) {
+        ids[rank] = (int32_t)(0xFFFFFFFFu - (uint32_t)q);
+        values[rank] = f.logprob(value_of((int)((uint32_t)(q >> 32) ^ 0x80000000u)));
+      });
+      for (int i = count + tid; i < a.top; i += kThreads) {
+        ids[i] = -1;
+        values[i] = -INFINITY;
+      }
+    }
+    return;
+  }
+  const int64_t slot = row * a.chunks + chunk;
+  if (tid == 0) *reinterpret_cast<float4*>(a.stats + 4 * slot) = make_float4(top, s, w, __int_as_float(min(count, a.top)));
+  if (kTop)
+    rank_candidates<kThreads>(place, count, a.top, [&](int rank, uint64_t q) {
+      a.best[slot * a.top + rank] = make_uint2((uint32_t)q, (uint32_t)(q >> 32));
+    });
+}
+
+// One workgroup per row joins its chunks.
+constexpr int kJoinThreads = 256;
+template <bool kBf16, bool kTop>
+__global__ __launch_bounds__(kJoinThreads) void k_logprobs_join(LogArgs a) {
+  __shared__ uint64_t place[kTop ? kMaxLogChunks * kMaxTop : 1];
+  __shared__ int counter;
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63;
+  if (kTop && tid == 0) counter = 0;
+  float4 part = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+  if (lane < a.chunks) part = *reinterpret_cast<const float4*>(a.stats + 4 * (row * a.chunks + lane));
+  const float top = value_of(wave_reduce<true>(order_of(part.x)));  // every wave has the row's
+  // S and W relative to the row's maximum
+  const float shift = part.x == -INFINITY ? 0.0f : (part.x - top) * a.c;
+  const float e = __builtin_amdgcn_exp2f(shift);
+  const float s = wave_sum(part.y * e), w = wave_sum(e * __builtin_fmaf(part.y, fmaxf(shift, -300.0f), part.z));
+  const Final f(a, top, s, w);
+  if (tid == 0) store_row<kBf16>(a, row, f);
+  if (!kTop) return;
+  // at least `top` are at or above the least of the chunks' r-th best
+  const int held = __float_as_int(part.w), r = (a.top + a.chunks - 1) / a.chunks;
+  int limit = INT_MAX;
+  if (lane < a.chunks) {
+    limit = INT_MIN;
+    if (held >= r) limit = (int)(a.best[(row * a.chunks + lane) * a.top + r - 1].y ^ 0x80000000u);
+  }
+  limit = -wave_reduce<true>(-max(limit, -INT_MAX));
+  __syncthreads();
+  for (int i = tid; i < a.chunks * a.top; i += kJoinThreads) {
+    const int chunk = i / a.top, at = i - chunk * a.top;
+    if (at >= __float_as_int(a.stats[4 * (row * a.chunks + chunk) + 3])) continue;
+    const uint2 q = a.best[row * a.chunks * a.top + i];
+    if ((int)(q.y ^ 0x80000000u) >= limit) place[atomicAdd(&counter, 1)] = (uint64_t)q.y << 32 | q.x;
+  }
+  __syncthreads();
+  const int count = counter;
+  int32_t* ids = a.top_id + row * a.top;
+  float* values = a.top_logprob + row * a.top;
+  rank_candidates<kJoinThreads>(place, count, a.top, [&](int rank, uint64_t q) {
+    ids[rank] = (int32_t)(0xFFFFFFFFu - (uint32_t)q);
+    values[rank] = f.logprob(value_of((int)((uint32_t)(q >> 32) ^ 0x80000000u)));
+  });
+  for (int i = count + tid; i < a.top; i += kJoinThreads) {
+    ids[i] = -1;
+    values[i] = -INFINITY;
+  }
+}
+
+// ---- gradient ----
+//   dx_j = scale * (g [j = t] + p_j (gz - g - gh (log p_j + H)))
+// with p_j = 2^d, d = fma(x_j, scale, -lse) log2 e.  Rows whose gradients are all
+// zero, and rows where nothing is possible, get zeros without being read.
+struct GradArgs {
+  const char* x;
+  int64_t x_stride;
+  char* dx;
+  int64_t dx_stride;
+  int n, chunks;
+  float scale;
+  const int32_t* target;
+  const float *lse, *entropy, *g, *gh, *gz;
+};
+
+constexpr int kGradThreads = 256;
+template <bool kBf16, int E, bool kAligned>
+__global__ __launch_bounds__(kGradThreads) void k_logprobs_backward(GradArgs a) {
+  typedef Pieces<kBf16> P;
+  constexpr int kPer = P::kPer;
+  const int64_t row = blockIdx.x / a.chunks;
+  const int chunk = (int)(blockIdx.x - row * a.chunks), tid = threadIdx.x;
+  const P p(a.x, a.x_stride, row, a.n);
+  const int per = (p.vecs + a.chunks - 1) / a.chunks, v0 = min(chunk * per, p.vecs), v1 = min(v0 + per, p.vecs);
+  const int t = a.target ? a.target[row] : -1;
+  const float lse = a.lse[row];
+  const float g = a.g && (uint32_t)t < (uint32_t)a.n ? a.g[row] : 0.0f;
+  const float gh = a.gh ? a.gh[row] : 0.0f, gz = a.gz ? a.gz[row] : 0.0f;
+  const bool zero = lse == -INFINITY || (g == 0.0f && gh == 0.0f && gz == 0.0f);
+  const float plain = a.scale * (gz - g - (gh != 0.0f ? gh * a.entropy[row] : 0.0f)), slope = -a.scale * gh * kLn2;
+  const float hit = zero ? 0.0f : a.scale * g;
+  char* out = a.dx + row * a.dx_stride;
+  auto value = [&](float x) {
+    const float d = __builtin_fmaf(x, a.scale, -lse) * kLog2e;
+    return __builtin_amdgcn_exp2f(d) * __builtin_fmaf(slope, fmaxf(d, -300.0f), plain);
+  };
+  auto store = [&](int j, float v) {
+    if (kBf16)
+      reinterpret_cast<uint16_t*>(out)[j] = f32_to_bf16_rne(v);
+    else
+      reinterpret_cast<float*>(out)[j] = v;
+  };
+  if (chunk == 0 && tid < p.edges()) {
+    const int j = p.edge(tid);
+    store(j, (zero ? 0.0f : value(p.at(j))) + (j == t ? hit : 0.0f));
+  }
+  v4u data[E];
+  if (!zero && v0 < v1) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) data[i] = *p.vec(min(v0 + i * kGradThreads + tid, v1 - 1));
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int v = v0 + i * kGradThreads + tid, first = p.head + v * kPer;
+    if (v >= v1) continue;
+    float y[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) y[j] = zero ? 0.0f : value(element<kBf16>(data[i], j));
+    if ((uint32_t)(t - first) < (uint32_t)kPer) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) y[j] += first + j == t ? hit : 0.0f;
+    }
+    if (kAligned) {
+      v4u w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = kBf16 ? f32x2_to_bf16x2(y[2 * j % kPer], y[(2 * j + 1) % kPer]) : __float_as_uint(y[j]);
+      *reinterpret_cast<v4u*>(out + (int64_t)first * P::kSize) = w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) store(first + j, y[j]);
+    }
+  }
+}
+
+// Vectors of 16 bytes per thread: as many as registers hold (8) while the rows
+// still give the chip two workgroups per CU, fewer for few rows.
+// A row has never more chunks than the joining workgroup holds.
+int vectors_per_thread(int64_t m, int64_t n, int per) {
+  const int64_t vecs = (n + per - 1) / per;
+  auto chunks = [&](int e) { return (vecs + e * kThreads - 1) / (e * kThreads); };
+  int e = 8;
+  while (e > 1 && m * chunks(e) < 512 && chunks(e / 2) <= kMaxLogChunks) e >>= 1;
+  return e;
+}
+
+struct LogPlan {
+  int e;
+  int64_t chunks;
+};
+LogPlan log_plan(int64_t m, int64_t n, bool bf16) {
+  const int per = bf16 ? 8 : 4;
+  LogPlan p;
+  p.e = vectors_per_thread(m, n, per);
+  const int64_t vecs = (n + per - 1) / per, hold = (int64_t)p.e * kThreads;
+  p.chunks = (vecs + hold - 1) / hold;
+  return p;
+}
+
+}  // namespace
+
+size_t logprobs_workspace_bytes(int64_t m, int64_t n, bool bf16, int64_t top) {
+  const LogPlan p = log_plan(m, n, bf16);
+  return p.chunks == 1 ? 0 : (size_t)(m * p.chunks) * (16 + 8 * (size_t)top);
+}
+
+hipError_t launch_logprobs(const void* x, bool bf16, int64_t m, int64_t n, int64_t stride, float scale,
+                           const int32_t* target, int64_t top, float* logprob, float* lse, float* entropy, int32_t* top_id,
+                           float* top_logprob, void* workspace, hipStream_t s) {
+  const LogPlan p = log_plan(m, n, bf16);
+  if (!grid_fits(m * p.chunks, kThreads)) return kErrGridTooLarge;
+  LogArgs a = {(const char*)x, stride * (bf16 ? 2 : 4), (int)n,      (int)p.chunks, (int)top, scale, scale * kLog2e,
+               target,         logprob,                 lse,     entropy,       top_id,   top_logprob};
+  a.stats = (float*)workspace;
+  a.best = (uint2*)(a.stats + 4 * m * p.chunks);
+  auto go = [&](auto b, auto e, auto with_top) {
+    constexpr bool kBf16 = decltype(b)::value, kTop = decltype(with_top)::value;
+    hipLaunchKernelGGL((k_logprobs<kBf16, decltype(e)::value, kTop>), dim3((unsigned)(m * p.chunks)), dim3(kThreads), 0, s, a);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess || p.chunks == 1) return err;
+    hipLaunchKernelGGL((k_logprobs_join<kBf16, kTop>), dim3((unsigned)m), dim3(kJoinThreads), 0, s, a);
+    return hipGetLastError();
+  };
+  using std::bool_constant;
+  using std::integral_constant;
+  auto by_e = [&](auto b, auto with_top) {
+    switch (p.e) {
+      case 1: return go(b, integral_constant<int, 1>{}, with_top);
+      case 2: return go(b, integral_constant<int, 2>{}, with_top);
+      case 4: return go(b, integral_constant<int, 4>{}, with_top);
+      default: return go(b, integral_constant<int, 8>{}, with_top);
+    }
+  };
+  auto by_top = [&](auto b) { return top > 0 ? by_e(b, bool_constant<true>{}) : by_e(b, bool_constant<false>{}); };
+  return bf16 ? by_top(bool_constant<true>{}) : by_top(bool_constant<false>{});
+}
+
+hipError_t launch_logprobs_backward(const void* x, bool bf16, int64_t m, int64_t n, int64_t stride, float scale,
+                                    const int32_t* target, const float* lse, const float* entropy, const float* g,
+                                    const float* gh, const float* gz, void* dx, int64_t dx_stride, hipStream_t s) {
+  constexpr int E = 4;
+  const int size = bf16 ? 2 : 4, per = 16 / size;
+  const int64_t vecs = (n + per - 1) / per, chunks = (vecs + E * kGradThreads - 1) / (E * kGradThreads);
+  if (!grid_fits(m * chunks, kGradThreads)) return kErrGridTooLarge;
+  const GradArgs a = {(const char*)x, stride * size, (char*)dx, dx_stride * size, (int)n, (int)chunks, scale,
+                      target,         lse,           entropy,   g,                gh,     gz};
+  // rows of both begin alike within 16 bytes: whole pieces of one are whole pieces of the other
+  const bool aligned = ((intptr_t)x - (intptr_t)dx) % 16 == 0 && (m == 1 || (stride - dx_stride) * size % 16 == 0);
+  const dim3 grid((unsigned)(m * chunks)), block(kGradThreads);
+  if (bf16) {
+    if (aligned)
+      hipLaunchKernelGGL((k_logprobs_backward<true, E, true>), grid, block, 0, s, a);
+    else
+      hipLaunchKernelGGL((k_logprobs_backward<true, E, false>), grid, block, 0, s, a);
+  } else {
+    if (aligned)
+      hipLaunchKernelGGL((k_logprobs_backward<false, E, true>), grid, block, 0, s, a);
+    else
+      hipLaunchKernelGGL((k_logprobs_backward<false, E, false>), grid, block, 0, s, a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace bl
