@@ -587,6 +587,37 @@ bl_status bl_kv_compact(const bl_kv_pool* pool, int32_t* table, int64_t table_st
 bl_status bl_kv_copy(const bl_kv_cache* caches, int64_t count, const int32_t* copies, int64_t n, const int32_t* valid,
                      void* stream);
 
+/* Sequences that begin alike: sequences group[g] .. group[g + 1] - 1 share
+ * their first prefix[g] tokens, which the pages of the first of them hold (the
+ * others' entries for them need not name the same pages, if theirs hold the
+ * same tokens).  No prefix[g] passes the start of one of its sequences.
+ * max_group bounds group[g + 1] - group[g], max_prefix the prefixes.  Values
+ * that break these bounds give no error and no access outside a buffer: they
+ * are taken as inside them; sequences in no group are left out. */
+typedef struct bl_kv_shared {
+    const int32_t* group;  /* device [groups + 1], ascending from 0 to seqs */
+    const int32_t* prefix; /* device [groups]                               */
+    int64_t groups;
+    int64_t max_group;
+    int64_t max_prefix;
+} bl_kv_shared;
+
+/* Device workspace of bl_attention_shared (0: an argument is invalid, or there is nothing to do). */
+size_t bl_attention_shared_workspace_bytes(const bl_kv_cache* cache, const bl_kv_batch* batch,
+                                           const bl_kv_shared* shared, int64_t q_heads);
+
+/* bl_attention without a window for such a batch: the keys and values of a
+ * prefix are read for all queries of its group together.  The results are
+ * those of bl_attention but for the order of the sums.  (A window leaves little
+ * of a long prefix to see: bl_attention reads no more than that.)
+ *   q, out, lse  as for bl_attention.
+ * Errors: BL_ERR_NULL, BL_ERR_SHAPE (also groups * max_group below seqs, a
+ * max_prefix past max_len), BL_ERR_ALIGN, BL_ERR_WORKSPACE, BL_ERR_HIP. */
+bl_status bl_attention_shared(const bl_kv_cache* cache, const bl_kv_batch* batch, const bl_kv_shared* shared,
+                              const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads,
+                              float scale, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
 /* ---- Log probabilities ----
  * Of the rows of logits x [m][n], with z_j = scale * x_j:
  *   lse = log sum_j exp z_j,   logprob = z_t - lse  for the given token t,

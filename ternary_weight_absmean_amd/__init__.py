@@ -27,7 +27,7 @@ __all__ = [
     "bl_rmsnorm_quant", "bl_rmsnorm_backward_workspace_bytes", "bl_rmsnorm_backward", "bl_rope_frequencies", "bl_rope",
     "Rope", "KVCache", "KVBatch", "bl_kv_append", "bl_kv_read", "bl_attention_workspace_bytes", "bl_attention",
     "KVPool", "KVCaches", "bl_kv_grow", "bl_kv_fork", "bl_kv_free", "bl_kv_compact_workspace_bytes", "bl_kv_compact",
-    "bl_kv_copy", "bl_logprobs_workspace_bytes", "bl_logprobs", "bl_logprobs_backward",
+    "bl_kv_copy", "KVShared", "bl_attention_shared_workspace_bytes", "bl_attention_shared", "bl_logprobs_workspace_bytes", "bl_logprobs", "bl_logprobs_backward",
 ]
 
 
@@ -114,6 +114,10 @@ _lib.bl_kv_compact.argtypes = [_P, _P, _I64, _I64, _I64, _P, _P, _P, _SZ, _P]
 _lib.bl_kv_compact.restype = _INT
 _lib.bl_kv_copy.argtypes = [_P, _I64, _P, _I64, _P, _P]
 _lib.bl_kv_copy.restype = _INT
+_lib.bl_attention_shared_workspace_bytes.argtypes = [_P, _P, _P, _I64]
+_lib.bl_attention_shared_workspace_bytes.restype = _SZ
+_lib.bl_attention_shared.argtypes = [_P, _P, _P, _P, _I64, _I64, _I64, _F32, _P, _P, _P, _SZ, _P]
+_lib.bl_attention_shared.restype = _INT
 _lib.bl_logprobs_workspace_bytes.argtypes = [_I64, _I64, _INT, _I64]
 _lib.bl_logprobs_workspace_bytes.restype = _SZ
 _lib.bl_logprobs.argtypes = [_P, _INT, _I64, _I64, _I64, _F32, _P, _I64, _P, _P, _P, _P, _P, _P, _SZ, _P]
@@ -822,6 +826,49 @@ def bl_kv_copy(caches: KVCaches | KVCache, copies: torch.Tensor, count: torch.Te
     many = len(caches) if isinstance(caches, KVCaches) else 1
     _check("bl_kv_copy", _lib.bl_kv_copy(caches.address, many, _dense(copies, "copies", torch.int32, (n, 3)), n,
                                          _dense(count, "count", torch.int32, (1,)), _stream(copies.device)))
+
+
+class KVShared:
+    """Sequences of a batch that begin alike: int32 device tensors ``group`` [groups + 1] (sequences group[g] ..
+    group[g + 1] - 1 share their beginning) and ``prefix`` [groups] (how many tokens); ``max_group`` and
+    ``max_prefix`` bound a group's sequences and the shared tokens."""
+
+    class _Struct(ctypes.Structure):
+        _fields_ = [("group", _P), ("prefix", _P), ("groups", _I64), ("max_group", _I64), ("max_prefix", _I64)]
+
+    def __init__(self, group: torch.Tensor, prefix: torch.Tensor, max_group: int, max_prefix: int):
+        _need(prefix, "prefix", torch.int32)
+        if prefix.dim() != 1:
+            raise ValueError(f"prefix must have shape (groups,), got {tuple(prefix.shape)}")
+        _need(group, "group", torch.int32, (prefix.shape[0] + 1,))
+        self.group, self.prefix = group, prefix
+        self.max_group, self.max_prefix = int(max_group), int(max_prefix)
+        self.struct = KVShared._Struct(group.data_ptr(), prefix.data_ptr(), prefix.shape[0], self.max_group, self.max_prefix)
+        self.address = ctypes.addressof(self.struct)
+
+
+def bl_attention_shared_workspace_bytes(cache: KVCache, batch: KVBatch, shared: KVShared, q_heads: int) -> int:
+    return int(_lib.bl_attention_shared_workspace_bytes(cache.address, batch.address, shared.address, q_heads))
+
+
+def bl_attention_shared(cache: KVCache, batch: KVBatch, shared: KVShared, q: torch.Tensor, scale: float | None = None,
+                        out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """bl_attention (without a window) of sequences that share prefixes, each of which is read once per group."""
+    q_heads = q.shape[1]
+    shape = (batch.tokens, q_heads, cache.dim)
+    qp, qt, qh = _heads(q, "q", shape)
+    if scale is None:
+        scale = cache.dim ** -0.5
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    if workspace is None:
+        nbytes = bl_attention_shared_workspace_bytes(cache, batch, shared, q_heads)
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+    _check("bl_attention_shared", _lib.bl_attention_shared(
+        cache.address, batch.address, shared.address, qp, qt, qh, q_heads, scale, _dense(out, "out", torch.bfloat16, shape),
+        _dense(lse, "lse", torch.float32, shape[:2]), workspace.data_ptr(), _bytes(workspace), _stream(q.device)))
+    return out
 
 
 _LOGIT_TYPES = {torch.bfloat16: 0, torch.float32: 1}

@@ -449,6 +449,52 @@ bl_status bl_attention(const bl_kv_cache* cache, const bl_kv_batch* batch, const
 
 namespace {
 
+// Groups cover the sequences, as far as the host can see.
+bl_status check_shared(const bl_kv_cache* cache, const bl_kv_batch* batch, const bl_kv_shared* shared, int64_t q_heads) {
+  if (bl_status st = check_kv(cache, batch)) return st;
+  if (!shared) return BL_ERR_NULL;
+  if (shared->groups < 0 || shared->groups > 65535 || shared->max_group < 0 || shared->max_group > 65535 ||
+      shared->max_prefix < 0 || shared->max_prefix > batch->max_len || shared->groups * shared->max_group < batch->seqs ||
+      !q_heads_ok(q_heads) || q_heads % cache->heads != 0 ||
+      shared->groups * shared->max_group > kMaxPositions / cache->heads ||
+      batch->tokens * (q_heads / cache->heads) > kMaxPositions)
+    return BL_ERR_SHAPE;
+  return BL_OK;
+}
+
+bl::KvGroups groups_of(const bl_kv_shared* s) { return {s->group, s->prefix, s->groups, s->max_group, s->max_prefix}; }
+
+}  // namespace
+
+size_t bl_attention_shared_workspace_bytes(const bl_kv_cache* cache, const bl_kv_batch* batch, const bl_kv_shared* shared,
+                                           int64_t q_heads) {
+  if (check_shared(cache, batch, shared, q_heads) != BL_OK || nothing_new(batch)) return 0;
+  return bl::attention_shared_workspace_bytes(view(cache), batch->tokens, batch->max_new, batch->max_len, q_heads,
+                                              groups_of(shared));
+}
+
+bl_status bl_attention_shared(const bl_kv_cache* cache, const bl_kv_batch* batch, const bl_kv_shared* shared,
+                              const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads,
+                              float scale, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  if (bl_status st = check_shared(cache, batch, shared, q_heads)) return st;
+  if (!(fabsf(scale) < INFINITY)) return BL_ERR_SHAPE;
+  if (nothing_new(batch)) return BL_OK;  // empty tensors may carry NULL pointers
+  if (!q || !out || !shared->group || !shared->prefix || !workspace) return BL_ERR_NULL;
+  if (!aligned(q, 16) || !strides_ok(q_token_stride, q_head_stride) || !aligned(out, 16) || !aligned(lse, 4) ||
+      !aligned(workspace, 16) || !aligned(shared->group, 4) || !aligned(shared->prefix, 4))
+    return BL_ERR_ALIGN;
+  const bl::KvView kv = view(cache);
+  const bl::KvGroups groups = groups_of(shared);
+  if (bl::attention_shared_workspace_bytes(kv, batch->tokens, batch->max_new, batch->max_len, q_heads, groups) > workspace_bytes)
+    return BL_ERR_WORKSPACE;
+  return from_hip(bl::launch_attention_shared(kv, step_of(batch), groups, batch->seqs, batch->tokens, batch->max_new,
+                                              batch->max_len, q, q_token_stride, q_head_stride, (int)q_heads, scale, out, lse,
+                                              workspace, (hipStream_t)stream));
+}
+
+namespace {
+
 // A pool, and a table of `seqs` rows that goes with it.
 bl_status check_pool(const bl_kv_pool* pool, int64_t seqs, int64_t stride) {
   if (!pool) return BL_ERR_NULL;

@@ -66,6 +66,18 @@ struct Attn {
   float* part_ml;  // [token][q_head][split][2]
 };
 
+// Sequences that share a prefix (bl_attention_shared): a group's queries take
+// its prefix together, as rows that all see all of it, in tiles of their own
+// (`pre`); the tiles of the single sequences then begin behind it.  Every row
+// leaves partial sums of both, which the join brings together.
+struct Shared : Attn {
+  const int32_t *of_group, *prefix;
+  int groups, max_group, max_prefix, seqs;
+  int pre_rows, pre_row_tiles, pre_tiles, pre_splits, pre_per;  // as tile_rows .. per
+  int pre_blocks;  // workgroups of this launch that take the prefixes; the others take the rest
+  int slots;       // partial sums per row: pre_splits + splits
+};
+
 // Wave-uniform values that nothing writes while the kernel runs (page numbers,
 // page scales), through scalar loads: a vector load of one would be waited for
 // together with all key and value loads in flight.
@@ -104,18 +116,21 @@ __host__ __device__ inline Span span_of(int first_pos, int last_pos, int max_len
 struct Tile : Span {
   int seq, head, begin, rows, row0, start;
   int first_pos, last_pos;  // positions of its first and last row
+  // of a Shared launch: whether it takes a prefix, its steps per split, its first partial sum
+  bool pre;
+  int per, slot;
 };
 
 // Workgroups are dealt to the eight XCDs in turn: eight tiles are taken
 // together, split by split, so that all splits of a tile run on one XCD and
 // every XCD gets tiles of all lengths.
-__device__ __forceinline__ bool tile_and_split(const Attn& a, int& index, int& split) {
+__device__ __forceinline__ bool tile_and_split(const Attn& a, uint32_t block, int& index, int& split) {
   if (a.tiles < 64) {  // too few to spread by eights
-    index = blockIdx.x / a.splits;
-    split = blockIdx.x - index * a.splits;
+    index = block / a.splits;
+    split = block - index * a.splits;
     return index < a.tiles;
   }
-  const int eight = blockIdx.x / (8 * a.splits), rest = blockIdx.x - eight * 8 * a.splits;
+  const int eight = block / (8 * a.splits), rest = block - eight * 8 * a.splits;
   split = rest >> 3;
   index = eight * 8 + (rest & 7);
   return index < a.tiles;
@@ -139,6 +154,97 @@ __device__ __forceinline__ bool find_tile(const Attn& a, int index, Tile& t) {
   t.last_pos = t.start + (min(t.row0 + a.tile_rows, t.rows) - 1) / a.group;
   static_cast<Span&>(t) = span_of(t.first_pos, t.last_pos, a.max_len, a.window, a.sinks);
   return true;
+}
+
+// The sequences of group g, and the steps that they share.
+struct Group {
+  int first, end, steps;
+  __device__ Group(const Shared& a, int g) {
+    const int from = uniform_load(a.of_group + g), to = uniform_load(a.of_group + g + 1), tokens = uniform_load(a.prefix + g);
+    first = min(max(from, 0), a.seqs);
+    end = min(min(max(to, first), a.seqs), first + a.max_group);
+    steps = min(max(tokens, 0), a.max_prefix) / kStep;
+  }
+};
+
+// Tile `index` of the single sequences, behind what they share (there may be no step).
+__device__ __forceinline__ bool find_rest(const Shared& a, int index, Tile& t) {
+  const int list = index / a.row_tiles, member = list / a.kv.heads, g = member / a.max_group;
+  const Group group(a, g);
+  t.seq = group.first + member - g * a.max_group;
+  if (t.seq >= group.end) return false;
+  t.head = list - member * a.kv.heads;
+  const KvStep& st = a.st;
+  const int from = uniform_load(st.offsets + t.seq), to = uniform_load(st.offsets + t.seq + 1);
+  const int start = uniform_load(st.start + t.seq);
+  t.begin = st.begin_of(from);
+  const int count = st.count_of(t.begin, to);
+  t.rows = count * a.group;
+  t.row0 = (index - list * a.row_tiles) * a.tile_rows;
+  if (t.row0 >= t.rows) return false;
+  t.start = st.start_from(start);
+  t.first_pos = t.start + t.row0 / a.group;
+  t.last_pos = t.start + (min(t.row0 + a.tile_rows, t.rows) - 1) / a.group;
+  static_cast<Span&>(t) = span_of(t.first_pos, t.last_pos, a.max_len, 0, 0);
+  t.base = group.steps;
+  t.steps = max(t.steps - t.base, 0);
+  t.pre = false;
+  t.per = a.per;
+  t.slot = a.pre_splits;
+  return true;
+}
+
+// Tile `index` of the prefixes: up to tile rows of all queries of a group and head.
+__device__ __forceinline__ bool find_prefix(const Shared& a, int list, int row_tile, Tile& t) {
+  const int g = list / a.kv.heads;
+  const Group group(a, g);
+  if (group.first >= group.end || group.steps == 0) return false;
+  t.seq = group.first;
+  t.head = list - g * a.kv.heads;
+  const KvStep& st = a.st;
+  const int from = uniform_load(st.offsets + group.first), to = uniform_load(st.offsets + group.end);
+  t.begin = st.begin_of(from);
+  t.rows = (st.begin_of(max(to, t.begin)) - t.begin) * a.group;
+  t.row0 = row_tile * a.pre_rows;
+  if (t.row0 >= t.rows) return false;
+  t.keys = group.steps * kStep;
+  t.start = t.first_pos = t.last_pos = t.keys - 1;
+  t.sink_steps = t.base = 0;
+  t.steps = group.steps;
+  t.pre = true;
+  t.per = a.pre_per;
+  t.slot = 0;
+  return true;
+}
+
+// Tile and split of a workgroup; longest_first: the last tiles of all heads
+// before the others, so that they end about together.  The tiles of a prefix
+// that read the same keys are neighbours, an eighth of all on each XCD.
+__device__ __forceinline__ bool find_work(const Attn& a, bool longest_first, Tile& t, int& split) {
+  int index;
+  if (!tile_and_split(a, blockIdx.x, index, split)) return false;
+  if (longest_first) {
+    const int lists = a.tiles / a.row_tiles, back = index / lists;
+    index = (index - back * lists) * a.row_tiles + (a.row_tiles - 1 - back);
+  }
+  return find_tile(a, index, t);
+}
+__device__ __forceinline__ bool find_work(const Shared& a, bool longest_first, Tile& t, int& split) {
+  int index;
+  if ((int)blockIdx.x < a.pre_blocks) {
+    const int eighth = a.pre_blocks / 8;
+    index = (blockIdx.x & 7) * eighth + (blockIdx.x >> 3);
+    const int unit = __builtin_amdgcn_readfirstlane(index / a.pre_row_tiles);
+    const int list = __builtin_amdgcn_readfirstlane(unit / a.pre_splits);
+    split = unit - list * a.pre_splits;
+    return index < a.pre_tiles * a.pre_splits && find_prefix(a, list, index - unit * a.pre_row_tiles, t);
+  }
+  if (!tile_and_split(a, blockIdx.x - a.pre_blocks, index, split)) return false;
+  if (longest_first) {
+    const int lists = a.tiles / a.row_tiles, back = index / lists;
+    index = (index - back * lists) * a.row_tiles + (a.row_tiles - 1 - back);
+  }
+  return find_rest(a, index, t);
 }
 
 // Largest value over lanes l and l ^ 32: v_permlane32_swap of a register with
@@ -251,18 +357,23 @@ constexpr float kSlack = 1.5f;
 // chain of page number, keys, products, meeting of the waves, join.
 // kPages: pages that 64 tokens lie in (1, or 4 for pages of 16 and
 // 32 tokens, looked up for each 16 tokens).
-template <int DC, int kPages>
-__global__ __launch_bounds__(kThreads, DC == 1 ? 4 : DC == 2 ? (kPages == 1 ? 3 : 2) : 1) void k_attn(Attn a) {
+template <int DC, int kPages, typename Args>
+__global__ __launch_bounds__(kThreads, DC == 1 ? 4 : DC == 2 ? (kPages == 1 ? 3 : 2) : 1) void k_attn(Args a) {
+  constexpr bool kShared = std::is_same<Args, Shared>::value;
   typedef typename VBytes<DC>::type vbytes;
+  const int window = kShared ? 0 : a.window, sinks = kShared ? 0 : a.sinks;
   __shared__ float lds_o[kWaves][16][64 * DC + 4];  // rows four banks apart
   __shared__ float lds_ml[kWaves][16][2];
-  int index, split;
-  if (!tile_and_split(a, index, split)) return;
+  int split;
   Tile t;
-  if (!find_tile(a, index, t)) return;
-  const int s0 = split * a.per, s1 = min(t.steps, s0 + a.per);
+  if (!find_work(a, false, t, split)) return;
+  const int per = kShared ? t.per : a.per, s0 = split * per, s1 = min(t.steps, s0 + per);
   if (s0 >= s1) return;
-  const bool whole = t.steps <= a.per;
+  const bool whole = !kShared && t.steps <= per;
+  if (kShared) {
+    for (int* v : {&t.seq, &t.head, &t.begin, &t.rows, &t.row0, &t.start, &t.first_pos, &t.keys, &t.base, &t.slot})
+      *v = __builtin_amdgcn_readfirstlane(*v);
+  }
 
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -270,7 +381,7 @@ __global__ __launch_bounds__(kThreads, DC == 1 ? 4 : DC == 2 ? (kPages == 1 ? 3 
   const bool valid = row < t.rows;
   const int token = valid ? row / a.group : 0;
   const int q_head = t.head * a.group + (valid ? row - token * a.group : 0);
-  const int pos = t.start + token, low = a.window > 0 ? pos - a.window + 1 : 0;
+  const int pos = t.start + (kShared && t.pre ? 0 : token), low = window > 0 ? pos - window + 1 : 0;
 
   // byte offsets inside a 16-token tile; elements past dim read element 0
   // instead (their query bytes are zero, their outputs are not stored)
@@ -349,7 +460,7 @@ __global__ __launch_bounds__(kThreads, DC == 1 ? 4 : DC == 2 ? (kPages == 1 ? 3 
     const bool more = step + kWaves < s1;
     float x[4][4], va[kPages];
     bool all = j0 + kStep <= min(t.first_pos + 1, t.keys) &&
-               (a.window == 0 || j0 > t.last_pos - a.window || j0 + kStep <= a.sinks);
+               (window == 0 || j0 > t.last_pos - window || j0 + kStep <= sinks);
 #pragma unroll
     for (int i = 0; i < kPages; ++i) {
       all = all && now.there[i];
@@ -378,7 +489,7 @@ __global__ __launch_bounds__(kThreads, DC == 1 ? 4 : DC == 2 ? (kPages == 1 ? 3 
     }
     if (!all) {
       asm volatile("; masked keys");  // stays a branch: most steps need none of this
-      const int at = j0 + 4 * g, past = min(pos, t.keys - 1) - at, before = low - at, first = a.sinks - at;
+      const int at = j0 + 4 * g, past = min(pos, t.keys - 1) - at, before = low - at, first = sinks - at;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -491,7 +602,8 @@ __global__ __launch_bounds__(kThreads, DC == 1 ? 4 : DC == 2 ? (kPages == 1 ? 3 
     if (a.lse && (tid & 15) == 0) a.lse[out_row] = sum != 0.0f ? (__log2f(sum) + top - 14.0f) * kLn2 : -INFINITY;
     return;
   }
-  const int64_t slot = out_row * a.splits + split;
+  int64_t slot = out_row * a.splits + split;
+  if constexpr (kShared) slot = out_row * a.slots + t.slot + split;
   if (seg < dim) {
     float4* dst = reinterpret_cast<float4*>(a.part_o + slot * dim + seg);
 #pragma unroll
@@ -559,8 +671,9 @@ struct VPiece<4> {
   static __device__ uint32_t word(type v, int c) { return v[c]; }
 };
 
-template <int DC, int kTeams>
-__global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_prompt(Attn a) {
+template <int DC, int kTeams, typename Args>
+__global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_prompt(Args a) {
+  constexpr bool kShared = std::is_same<Args, Shared>::value;
   typedef typename VPiece<DC>::type vpiece;
   constexpr int kTiles = 2 * DC;  // 32-element tiles of the head
   struct Ring {
@@ -569,17 +682,12 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
     float4 scale[kRing][4];           // per 16 tokens: ka, log2 va, 1 / va, there
   };
   __shared__ Ring rings[kTeams];
-  int index, split;
-  if (!tile_and_split(a, index, split)) return;
+  int split;
   Tile t;
-  {  // the longest (last) tiles of all heads first: they end about together
-    const int lists = a.tiles / a.row_tiles, back = index / lists;
-    index = (index - back * lists) * a.row_tiles + (a.row_tiles - 1 - back);
-  }
-  if (!find_tile(a, index, t)) return;
-  const int s0 = split * a.per, s1 = min(t.steps, s0 + a.per);
+  if (!find_work(a, true, t, split)) return;
+  const int per = kShared ? t.per : a.per, s0 = split * per, s1 = min(t.steps, s0 + per);
   if (s0 >= s1) return;
-  const bool whole = t.steps <= a.per;
+  const bool whole = !kShared && t.steps <= per;
 
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5, col = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane((tid >> 6) & 3), team = __builtin_amdgcn_readfirstlane(tid >> 8);
@@ -587,9 +695,10 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
   const bool busy = wave_row < t.rows, valid = row < t.rows;
   const int token = valid ? row / a.group : 0;
   const int q_head = t.head * a.group + (valid ? row - token * a.group : 0);
-  const int pos = t.start + token, low = a.window > 0 ? pos - a.window + 1 : 0;
-  const int first_pos = __builtin_amdgcn_readfirstlane(t.start + wave_row / a.group);
-  const int last_pos = __builtin_amdgcn_readfirstlane(t.start + (min(wave_row + 32, t.rows) - 1) / a.group);
+  const bool pre = kShared && t.pre;  // then all rows stand behind all keys
+  const int pos = pre ? t.start : t.start + token, low = a.window > 0 ? pos - a.window + 1 : 0;
+  const int first_pos = __builtin_amdgcn_readfirstlane(pre ? t.start : t.start + wave_row / a.group);
+  const int last_pos = __builtin_amdgcn_readfirstlane(pre ? t.start : t.start + (min(wave_row + 32, t.rows) - 1) / a.group);
   v16f o[kTiles];
 #pragma unroll
   for (int i = 0; i < kTiles; ++i)
@@ -688,7 +797,7 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
   // products and their softmax in turn 883 cycles, mixed 693).  Wave priorities:
   // staging, which other waves wait for, before the values' products before the
   // rest (6000 tokens, 20/5 heads: 223 us against 245 without; 6 x 509 under a
-  // window of 1024 52.7 against 55.8).
+  // a.window of 1024 52.7 against 55.8).
   v16i high, lo;   // the next half's scores
   v8h pf[2];       // the half before: its probabilities,
   uint4 vf[2][kTiles];  // and its values
@@ -866,7 +975,8 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
   if (!valid) return;
   const int64_t out_row = (int64_t)(t.begin + token) * a.q_heads + q_head;
   const float mul = l != 0.0f ? (512.0f / 127.0f) / l : 0.0f;
-  const int64_t slot = out_row * a.splits + split;
+  int64_t slot = out_row * a.splits + split;
+  if constexpr (kShared) slot = out_row * a.slots + t.slot + split;
   // o[i][4b + j] is element 2 DC (8b + 4g + j) + i: 8 DC adjacent ones per b
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
@@ -904,8 +1014,9 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
 // waves per row, whose lanes take four elements each and, 16 DC lanes apart,
 // different splits.  One wave per row for up to eight splits; four for more,
 // where a row's partial sums are a serial chain of loads otherwise.
-template <int DC, int kRowWaves>
-__global__ __launch_bounds__(kThreads) void k_attn_join(Attn a) {
+template <int DC, int kRowWaves, typename Args>
+__global__ __launch_bounds__(kThreads) void k_attn_join(Args a) {
+  constexpr bool kShared = std::is_same<Args, Shared>::value;
   constexpr int kRows = kWaves / kRowWaves, kLanes = 16 * DC, kGroups = 64 / kLanes;
   __shared__ v4f lds_x[kWaves][kLanes];
   __shared__ float lds_sum[kWaves];
@@ -913,14 +1024,25 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(Attn a) {
   const int pieces = a.tile_rows / kRows, tile = blockIdx.x / pieces;
   const int r = (blockIdx.x - tile * pieces) * kRows + wave / kRowWaves;
   Tile t;
-  if (!find_tile(a, tile, t) || t.steps <= a.per) return;
-  const int splits = (t.steps + a.per - 1) / a.per, row = t.row0 + r;
+  int splits, slots = a.splits, early = 0, skip = 0;  // of the slots, those from `early` on lie `skip` further
+  if constexpr (kShared) {
+    if (!find_rest(a, tile, t)) return;
+    early = (t.base + a.pre_per - 1) / a.pre_per;
+    skip = a.pre_splits - early;
+    splits = early + (t.steps + a.per - 1) / a.per;
+    slots = a.slots;
+  } else {
+    if (!find_tile(a, tile, t) || t.steps <= a.per) return;
+    splits = (t.steps + a.per - 1) / a.per;
+  }
+  auto place = [&](int i) { return kShared && i >= early ? i + skip : i; };
+  const int row = t.row0 + r;
   const bool valid = row < t.rows;
   const int tok = valid ? row / a.group : 0;
   const int64_t out_row = (int64_t)(t.begin + tok) * a.q_heads + t.head * a.group + (valid ? row - tok * a.group : 0);
-  const float* ml = a.part_ml + out_row * a.splits * 2;
+  const float* ml = a.part_ml + out_row * slots * 2;
   float top = kNone;
-  for (int i = lane; valid && i < splits; i += 64) top = fmaxf(top, ml[2 * i]);
+  for (int i = lane; valid && i < splits; i += 64) top = fmaxf(top, ml[2 * place(i)]);
   top = rows_max(top);
   for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
   const int at = (lane & (kLanes - 1)) * 4;
@@ -929,9 +1051,10 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(Attn a) {
 #pragma unroll 4
   for (int i = (wave % kRowWaves) * kGroups + lane / kLanes; i < splits; i += kRowWaves * kGroups) {
     if (!valid) break;
-    const float weight = __builtin_amdgcn_exp2f(ml[2 * i] - top);
-    const v4f f = *reinterpret_cast<const v4f*>(a.part_o + (out_row * a.splits + i) * dim + (at < dim ? at : 0));
-    sum = __builtin_fmaf(weight, ml[2 * i + 1], sum);
+    const int p = place(i);
+    const float weight = __builtin_amdgcn_exp2f(ml[2 * p] - top);
+    const v4f f = *reinterpret_cast<const v4f*>(a.part_o + (out_row * slots + p) * dim + (at < dim ? at : 0));
+    sum = __builtin_fmaf(weight, ml[2 * p + 1], sum);
 #pragma unroll
     for (int j = 0; j < 4; ++j) x[j] = __builtin_fmaf(weight, f[j], x[j]);
   }
@@ -1050,6 +1173,34 @@ int64_t most_splits(const KvView& kv, int64_t seqs, int64_t max_new, int64_t max
   return a > b ? a : b;
 }
 
+// Tiles and splits of a batch that shares prefixes: `pre` of the prefixes (a
+// group's queries together), `rest` of the single sequences behind them.
+struct SharedPlan {
+  Plan pre, rest;
+  int64_t slots() const { return pre.splits + rest.splits; }
+};
+
+SharedPlan make_shared_plan(const KvView& kv, int64_t tokens, int64_t max_new, int64_t max_len, int64_t q_heads,
+                            int64_t groups, int64_t max_group, int64_t max_prefix) {
+  SharedPlan p;
+  p.rest = make_plan(kv, groups * max_group, max_new, max_len, q_heads, 0, 0);
+  const int64_t most = max_group * max_new < tokens ? max_group * max_new : tokens;
+  const int64_t rows = most * (q_heads / kv.heads), lists = groups * kv.heads, steps = max_prefix / kStep;
+  Plan& pre = p.pre;
+  pre.tile_rows = rows < 64 ? 16 : kPromptRows;
+  pre.row_tiles = (rows + pre.tile_rows - 1) / pre.tile_rows;
+  pre.tiles = lists * pre.row_tiles;
+  pre.teams = 1;
+  pre.splits = pre.per = 1;
+  if (steps == 0) return p;
+  const int64_t target = pre.tile_rows == 16 ? 1024 : kTargetPromptBlocks;
+  const int64_t wanted = pre.tiles < target ? target / pre.tiles : 1, limit = (steps + kWaves - 1) / kWaves;
+  const int64_t splits = wanted < limit ? wanted : limit;
+  pre.per = (int)((steps + splits - 1) / splits);
+  pre.splits = (int)((steps + pre.per - 1) / pre.per);
+  return p;
+}
+
 }  // namespace
 
 size_t attention_workspace_bytes(const KvView& kv, int64_t seqs, int64_t tokens, int64_t max_new, int64_t max_len,
@@ -1091,27 +1242,120 @@ hipError_t launch_attention(const KvView& kv, const KvStep& st, int64_t seqs, in
     auto prompt = [&](int teams) {
       if constexpr (DC <= 2) {
         if (teams == 2) {
-          hipLaunchKernelGGL((k_attn_prompt<DC, 2>), dim3((unsigned)blocks), dim3(2 * kThreads), 0, s, a);
+          hipLaunchKernelGGL((k_attn_prompt<DC, 2, Attn>), dim3((unsigned)blocks), dim3(2 * kThreads), 0, s, a);
           return;
         }
       }
-      hipLaunchKernelGGL((k_attn_prompt<DC, 1>), dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
+      hipLaunchKernelGGL((k_attn_prompt<DC, 1, Attn>), dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
     };
     const dim3 grid((unsigned)blocks);
     if (p.tile_rows == 16) {
       if (kv.page_tokens >= kStep)
-        hipLaunchKernelGGL((k_attn<DC, 1>), grid, dim3(kThreads), 0, s, a);
+        hipLaunchKernelGGL((k_attn<DC, 1, Attn>), grid, dim3(kThreads), 0, s, a);
       else
-        hipLaunchKernelGGL((k_attn<DC, 4>), grid, dim3(kThreads), 0, s, a);
+        hipLaunchKernelGGL((k_attn<DC, 4, Attn>), grid, dim3(kThreads), 0, s, a);
     } else {
       prompt(p.teams);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits <= 1) return e;
     if (p.splits <= 8)
-      hipLaunchKernelGGL((k_attn_join<DC, 1>), dim3((unsigned)(p.tiles * (p.tile_rows / kWaves))), dim3(kThreads), 0, s, a);
+      hipLaunchKernelGGL((k_attn_join<DC, 1, Attn>), dim3((unsigned)(p.tiles * (p.tile_rows / kWaves))), dim3(kThreads), 0, s, a);
     else
-      hipLaunchKernelGGL((k_attn_join<DC, kWaves>), dim3((unsigned)(p.tiles * p.tile_rows)), dim3(kThreads), 0, s, a);
+      hipLaunchKernelGGL((k_attn_join<DC, kWaves, Attn>), dim3((unsigned)(p.tiles * p.tile_rows)), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+  };
+  if (kv.dim <= 64) return go(std::integral_constant<int, 1>{});
+  if (kv.dim <= 128) return go(std::integral_constant<int, 2>{});
+  return go(std::integral_constant<int, 4>{});
+}
+
+size_t attention_shared_workspace_bytes(const KvView& kv, int64_t tokens, int64_t max_new, int64_t max_len, int64_t q_heads,
+                                        const KvGroups& gr) {
+  const SharedPlan p = make_shared_plan(kv, tokens, max_new, max_len, q_heads, gr.groups, gr.max_group, gr.max_prefix);
+  return (size_t)tokens * (size_t)q_heads * (size_t)p.slots() * (size_t)(kv.dim + 2) * 4;
+}
+
+hipError_t launch_attention_shared(const KvView& kv, const KvStep& st, const KvGroups& gr, int64_t seqs, int64_t tokens,
+                                   int64_t max_new, int64_t max_len, const uint16_t* q, int64_t qt, int64_t qh, int q_heads,
+                                   float scale, uint16_t* out, float* lse, void* workspace, hipStream_t s) {
+  const SharedPlan p = make_shared_plan(kv, tokens, max_new, max_len, q_heads, gr.groups, gr.max_group, gr.max_prefix);
+  const Plan &pre = p.pre, &rest = p.rest;
+  const bool any = gr.max_prefix >= kStep;
+  const int64_t pre_blocks = any ? (pre.tiles * pre.splits + 7) / 8 * 8 : 0;
+  const int64_t rest_blocks = (rest.tiles + 7) / 8 * 8 * rest.splits;
+  if (!grid_fits(pre_blocks + rest_blocks, 2 * kThreads) || pre_blocks > 0x7FFFFFFF - 8 ||
+      !grid_fits(rest.tiles * rest.tile_rows, kThreads))
+    return kErrGridTooLarge;
+  Shared a;
+  a.kv = kv;
+  a.st = st;
+  a.q = q;
+  a.qt = qt;
+  a.qh = qh;
+  a.q_heads = q_heads;
+  a.group = q_heads / kv.heads;
+  a.page_shift = __builtin_ctz((unsigned)kv.page_tokens);
+  a.max_len = (int)max_len;
+  a.window = a.sinks = 0;
+  a.scale = scale * kLog2e;
+  a.tile_rows = rest.tile_rows;
+  a.row_tiles = (int)rest.row_tiles;
+  a.tiles = (int)rest.tiles;
+  a.splits = rest.splits;
+  a.per = rest.per;
+  a.out = out;
+  a.lse = lse;
+  a.slots = (int)p.slots();
+  a.part_o = (float*)workspace;
+  a.part_ml = a.part_o + tokens * q_heads * a.slots * kv.dim;
+  a.of_group = gr.group;
+  a.prefix = gr.prefix;
+  a.groups = (int)gr.groups;
+  a.max_group = (int)gr.max_group;
+  a.max_prefix = (int)gr.max_prefix;
+  a.seqs = (int)seqs;
+  a.pre_rows = pre.tile_rows;
+  a.pre_row_tiles = (int)pre.row_tiles;
+  a.pre_tiles = (int)pre.tiles;
+  a.pre_splits = pre.splits;
+  a.pre_per = pre.per;
+  auto go = [&](auto dc) {
+    constexpr int DC = decltype(dc)::value;
+    // the prefixes' workgroups and the others: one launch where the kernel is the same
+    auto launch = [&](int tile_rows, int teams, int64_t blocks_of_prefixes, int64_t blocks_of_rest) {
+      Shared b = a;
+      b.pre_blocks = (int)blocks_of_prefixes;
+      const dim3 grid((unsigned)(blocks_of_prefixes + blocks_of_rest));
+      if (tile_rows == 16) {
+        if (kv.page_tokens >= kStep)
+          hipLaunchKernelGGL((k_attn<DC, 1, Shared>), grid, dim3(kThreads), 0, s, b);
+        else
+          hipLaunchKernelGGL((k_attn<DC, 4, Shared>), grid, dim3(kThreads), 0, s, b);
+        return hipGetLastError();
+      }
+      if constexpr (DC <= 2) {
+        if (teams == 2) {
+          hipLaunchKernelGGL((k_attn_prompt<DC, 2, Shared>), grid, dim3(2 * kThreads), 0, s, b);
+          return hipGetLastError();
+        }
+      }
+      hipLaunchKernelGGL((k_attn_prompt<DC, 1, Shared>), grid, dim3(kThreads), 0, s, b);
+      return hipGetLastError();
+    };
+    hipError_t e;
+    if (pre_blocks > 0 && pre.tile_rows == rest.tile_rows && pre.teams == rest.teams) {
+      e = launch(rest.tile_rows, rest.teams, pre_blocks, rest_blocks);
+    } else {
+      e = pre_blocks > 0 ? launch(pre.tile_rows, pre.teams, pre_blocks, 0) : hipSuccess;
+      if (e == hipSuccess) e = launch(rest.tile_rows, rest.teams, 0, rest_blocks);
+    }
+    if (e != hipSuccess) return e;
+    if (a.slots <= 8)
+      hipLaunchKernelGGL((k_attn_join<DC, 1, Shared>), dim3((unsigned)(rest.tiles * (rest.tile_rows / kWaves))), dim3(kThreads), 0,
+                         s, a);
+    else
+      hipLaunchKernelGGL((k_attn_join<DC, kWaves, Shared>), dim3((unsigned)(rest.tiles * rest.tile_rows)), dim3(kThreads), 0, s, a);
     return hipGetLastError();
   };
   if (kv.dim <= 64) return go(std::integral_constant<int, 1>{});
