@@ -73,9 +73,13 @@ struct Attn {
 struct Shared : Attn {
   const int32_t *of_group, *prefix;
   int groups, max_group, max_prefix, seqs;
-  int pre_rows, pre_row_tiles, pre_tiles, pre_splits, pre_per;  // as tile_rows .. per
+  int pre_rows, pre_row_tiles, pre_tiles, pre_splits;  // as tile_rows .. splits
   int pre_blocks;  // workgroups of this launch that take the prefixes; the others take the rest
   int slots;       // partial sums per row: pre_splits + splits
+  int least, pre_least;  // steps of a split at least (the lengths are the device's)
+  bool finish;           // the prefixes' sums are there: a tile of one split joins them and is done
+  __device__ int steps_per_split(int steps) const { return max((steps + splits - 1) / splits, least); }
+  __device__ int pre_steps_per_split(int steps) const { return max((steps + pre_splits - 1) / pre_splits, pre_least); }
 };
 
 // Wave-uniform values that nothing writes while the kernel runs (page numbers,
@@ -189,7 +193,7 @@ __device__ __forceinline__ bool find_rest(const Shared& a, int index, Tile& t) {
   t.base = group.steps;
   t.steps = max(t.steps - t.base, 0);
   t.pre = false;
-  t.per = a.per;
+  t.per = a.steps_per_split(t.steps);
   t.slot = a.pre_splits;
   return true;
 }
@@ -212,7 +216,7 @@ __device__ __forceinline__ bool find_prefix(const Shared& a, int list, int row_t
   t.sink_steps = t.base = 0;
   t.steps = group.steps;
   t.pre = true;
-  t.per = a.pre_per;
+  t.per = a.pre_steps_per_split(t.steps);
   t.slot = 0;
   return true;
 }
@@ -369,7 +373,8 @@ __global__ __launch_bounds__(kThreads, DC == 1 ? 4 : DC == 2 ? (kPages == 1 ? 3 
   if (!find_work(a, false, t, split)) return;
   const int per = kShared ? t.per : a.per, s0 = split * per, s1 = min(t.steps, s0 + per);
   if (s0 >= s1) return;
-  const bool whole = !kShared && t.steps <= per;
+  bool whole = t.steps <= per;
+  if constexpr (kShared) whole &= a.finish && !t.pre;
   if (kShared) {
     for (int* v : {&t.seq, &t.head, &t.begin, &t.rows, &t.row0, &t.start, &t.first_pos, &t.keys, &t.base, &t.slot})
       *v = __builtin_amdgcn_readfirstlane(*v);
@@ -593,6 +598,29 @@ __global__ __launch_bounds__(kThreads, DC == 1 ? 4 : DC == 2 ? (kPages == 1 ? 3 
     for (int w = 0; w < kWaves; ++w) x[i] = __builtin_fmaf(weight[w], lds_o[w][r][seg + i], x[i]);
   }
   if (whole) {
+    if constexpr (kShared) {  // the prefix's splits
+      const int pre_per = a.pre_steps_per_split(t.base), early = (t.base + pre_per - 1) / pre_per;
+      const float* ml = a.part_ml + out_row * a.slots * 2;
+      const float* from = a.part_o + out_row * a.slots * dim + (seg < dim ? seg : 0);
+      float most = top;
+      for (int i = 0; i < early; ++i) most = fmaxf(most, ml[2 * i]);
+      const float keep = __builtin_amdgcn_exp2f(top - most);
+      sum *= keep;
+#pragma unroll
+      for (int i = 0; i < 4 * DC; ++i) x[i] *= keep;
+#pragma unroll 4
+      for (int i = 0; i < early; ++i) {
+        const float w = __builtin_amdgcn_exp2f(ml[2 * i] - most);
+        sum = __builtin_fmaf(w, ml[2 * i + 1], sum);
+#pragma unroll
+        for (int j = 0; j < DC; ++j) {
+          const v4f f = *reinterpret_cast<const v4f*>(from + i * dim + 4 * j);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[4 * j + k] = __builtin_fmaf(w, f[k], x[4 * j + k]);
+        }
+      }
+      top = most;
+    }
     const float mul = sum != 0.0f ? (512.0f / 127.0f) / sum : 0.0f;
     if (seg < dim) {
       uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + out_row * dim + seg);
@@ -1026,10 +1054,11 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(Args a) {
   Tile t;
   int splits, slots = a.splits, early = 0, skip = 0;  // of the slots, those from `early` on lie `skip` further
   if constexpr (kShared) {
-    if (!find_rest(a, tile, t)) return;
-    early = (t.base + a.pre_per - 1) / a.pre_per;
+    if (!find_rest(a, tile, t) || (a.finish && t.steps <= t.per)) return;
+    const int pre_per = a.pre_steps_per_split(t.base);
+    early = (t.base + pre_per - 1) / pre_per;
     skip = a.pre_splits - early;
-    splits = early + (t.steps + a.per - 1) / a.per;
+    splits = early + (t.steps + t.per - 1) / t.per;
     slots = a.slots;
   } else {
     if (!find_tile(a, tile, t) || t.steps <= a.per) return;
@@ -1081,6 +1110,57 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(Args a) {
     *reinterpret_cast<uint2*>(a.out + out_row * dim + at) =
         make_uint2(f32x2_to_bf16x2(x[0] * mul, x[1] * mul), f32x2_to_bf16x2(x[2] * mul, x[3] * mul));
   if (a.lse && lane == 0) a.lse[out_row] = sum != 0.0f ? (__log2f(sum) + top - 14.0f) * kLn2 : -INFINITY;
+}
+
+// Joins a prefix and a rest of few splits (up to eight): 16 DC lanes take a row,
+// four elements each, and all its splits, four at a time, so that a wave has
+// the loads of several rows in flight.  33000 rows of two splits: 10 us, 24 with a wave per row.
+template <int DC>
+__global__ __launch_bounds__(kThreads) void k_attn_join_few(Shared a) {
+  constexpr int kLanes = 16 * DC, kRows = kThreads / kLanes, kTogether = 4;
+  const int tid = threadIdx.x, dim = a.kv.dim;
+  const int pieces = a.tile_rows / kRows, tile = blockIdx.x / pieces;
+  Tile t;
+  if (!find_rest(a, tile, t) || (a.finish && t.steps <= t.per)) return;
+  const int row = t.row0 + (blockIdx.x - tile * pieces) * kRows + tid / kLanes, at = (tid % kLanes) * 4;
+  if (row >= t.rows) return;
+  const int tok = row / a.group;
+  const int64_t out_row = (int64_t)(t.begin + tok) * a.q_heads + t.head * a.group + (row - tok * a.group);
+  const int pre_per = a.pre_steps_per_split(t.base), early = (t.base + pre_per - 1) / pre_per;
+  const int splits = early + (t.steps + t.per - 1) / t.per;
+  const float* ml = a.part_ml + out_row * a.slots * 2;
+  const float* from = a.part_o + out_row * a.slots * dim + (at < dim ? at : 0);
+  float top = kNone, sum = 0.0f;
+  v4f x = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i0 = 0; i0 < splits; i0 += kTogether) {
+    float2 stat[kTogether];
+    v4f f[kTogether];
+    float most = top;
+#pragma unroll
+    for (int j = 0; j < kTogether; ++j) {
+      const int i = min(i0 + j, splits - 1), p = i < early ? i : i - early + a.pre_splits;
+      stat[j] = *reinterpret_cast<const float2*>(ml + 2 * p);
+      f[j] = *reinterpret_cast<const v4f*>(from + (int64_t)p * dim);
+    }
+#pragma unroll
+    for (int j = 0; j < kTogether; ++j) most = fmaxf(most, stat[j].x);
+    const float keep = __builtin_amdgcn_exp2f(top - most);
+    sum *= keep;
+    x *= keep;
+#pragma unroll
+    for (int j = 0; j < kTogether; ++j) {
+      const float w = i0 + j < splits ? __builtin_amdgcn_exp2f(stat[j].x - most) : 0.0f;
+      if (i0 + j < splits) sum = __builtin_fmaf(w, stat[j].y, sum);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = i0 + j < splits ? __builtin_fmaf(w, f[j][k], x[k]) : x[k];
+    }
+    top = most;
+  }
+  const float mul = sum != 0.0f ? (512.0f / 127.0f) / sum : 0.0f;
+  if (at < dim)
+    *reinterpret_cast<uint2*>(a.out + out_row * dim + at) =
+        make_uint2(f32x2_to_bf16x2(x[0] * mul, x[1] * mul), f32x2_to_bf16x2(x[2] * mul, x[3] * mul));
+  if (a.lse && at == 0) a.lse[out_row] = sum != 0.0f ? (__log2f(sum) + top - 14.0f) * kLn2 : -INFINITY;
 }
 
 // Workgroups along the keys: enough to fill the chip, none with less than a
@@ -1174,30 +1254,44 @@ int64_t most_splits(const KvView& kv, int64_t seqs, int64_t max_new, int64_t max
 }
 
 // Tiles and splits of a batch that shares prefixes: `pre` of the prefixes (a
-// group's queries together), `rest` of the single sequences behind them.
+// group's queries together), `rest` of the single sequences behind them.  The
+// host knows the longest prefix and the longest sequence, not what lies between
+// them in one sequence: a tile spreads its own steps over the planned splits.
+// finish: the rest runs behind the prefixes, in a launch of its own, and joins
+// them itself where its tile is one split; otherwise both are one launch, if
+// their kernel is the same, and the join another.
 struct SharedPlan {
   Plan pre, rest;
-  int64_t slots() const { return pre.splits + rest.splits; }
+  bool finish;
+  int64_t slots() const { return pre.splits + (finish && rest.splits == 1 ? 0 : rest.splits); }
 };
+
+constexpr int64_t kSharedBlocks = 512;
 
 SharedPlan make_shared_plan(const KvView& kv, int64_t tokens, int64_t max_new, int64_t max_len, int64_t q_heads,
                             int64_t groups, int64_t max_group, int64_t max_prefix) {
   SharedPlan p;
-  p.rest = make_plan(kv, groups * max_group, max_new, max_len, q_heads, 0, 0);
+  Plan &pre = p.pre, &rest = p.rest;
+  const int64_t group = q_heads / kv.heads, steps = (max_len + kStep - 1) / kStep, pre_steps = max_prefix / kStep;
+  auto pick = [](int64_t tiles, int64_t blocks, int64_t steps, int64_t least) {
+    const int64_t wanted = tiles < blocks ? blocks / tiles : 1, most = (steps + least - 1) / least;
+    return (int)(wanted < most ? wanted : most > 1 ? most : 1);
+  };
+  const int64_t lists = groups * max_group * kv.heads, rows = max_new * group;
+  rest.tile_rows = few_rows(rows, lists, steps - pre_steps, kv.dim) ? 16 : kPromptRows;
+  rest.row_tiles = (rows + rest.tile_rows - 1) / rest.tile_rows;
+  rest.tiles = lists * rest.row_tiles;
   const int64_t most = max_group * max_new < tokens ? max_group * max_new : tokens;
-  const int64_t rows = most * (q_heads / kv.heads), lists = groups * kv.heads, steps = max_prefix / kStep;
-  Plan& pre = p.pre;
-  pre.tile_rows = rows < 64 ? 16 : kPromptRows;
-  pre.row_tiles = (rows + pre.tile_rows - 1) / pre.tile_rows;
-  pre.tiles = lists * pre.row_tiles;
-  pre.teams = 1;
-  pre.splits = pre.per = 1;
-  if (steps == 0) return p;
-  const int64_t target = pre.tile_rows == 16 ? 1024 : kTargetPromptBlocks;
-  const int64_t wanted = pre.tiles < target ? target / pre.tiles : 1, limit = (steps + kWaves - 1) / kWaves;
-  const int64_t splits = wanted < limit ? wanted : limit;
-  pre.per = (int)((steps + splits - 1) / splits);
-  pre.splits = (int)((steps + pre.per - 1) / pre.per);
+  pre.tile_rows = most * group < 64 ? 16 : kPromptRows;
+  pre.row_tiles = (most * group + pre.tile_rows - 1) / pre.tile_rows;
+  pre.tiles = groups * kv.heads * pre.row_tiles;
+  p.finish = rest.tile_rows == 16 && (pre.tile_rows != 16 || pre_steps == 0);
+  const int64_t all = p.finish ? pre.tiles : pre.tiles + rest.tiles;
+  pre.teams = pre.tile_rows != 16 && kv.dim <= 128 && all < 256 ? 2 : 1;
+  rest.teams = rest.tile_rows != 16 ? pre.teams : 1;
+  rest.splits = pick(rest.tiles, kSharedBlocks / rest.teams, steps, kWaves);
+  pre.splits = pick(pre.tiles, kSharedBlocks / pre.teams, pre_steps, kWaves);
+  pre.per = rest.per = kWaves;
   return p;
 }
 
@@ -1303,7 +1397,7 @@ hipError_t launch_attention_shared(const KvView& kv, const KvStep& st, const KvG
   a.row_tiles = (int)rest.row_tiles;
   a.tiles = (int)rest.tiles;
   a.splits = rest.splits;
-  a.per = rest.per;
+  a.per = a.least = rest.per;
   a.out = out;
   a.lse = lse;
   a.slots = (int)p.slots();
@@ -1319,7 +1413,8 @@ hipError_t launch_attention_shared(const KvView& kv, const KvStep& st, const KvG
   a.pre_row_tiles = (int)pre.row_tiles;
   a.pre_tiles = (int)pre.tiles;
   a.pre_splits = pre.splits;
-  a.pre_per = pre.per;
+  a.pre_least = pre.per;
+  a.finish = p.finish;
   auto go = [&](auto dc) {
     constexpr int DC = decltype(dc)::value;
     // the prefixes' workgroups and the others: one launch where the kernel is the same
@@ -1344,16 +1439,16 @@ hipError_t launch_attention_shared(const KvView& kv, const KvStep& st, const KvG
       return hipGetLastError();
     };
     hipError_t e;
-    if (pre_blocks > 0 && pre.tile_rows == rest.tile_rows && pre.teams == rest.teams) {
+    if (pre_blocks > 0 && pre.tile_rows == rest.tile_rows) {
       e = launch(rest.tile_rows, rest.teams, pre_blocks, rest_blocks);
     } else {
       e = pre_blocks > 0 ? launch(pre.tile_rows, pre.teams, pre_blocks, 0) : hipSuccess;
       if (e == hipSuccess) e = launch(rest.tile_rows, rest.teams, 0, rest_blocks);
     }
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || (p.finish && rest.splits == 1)) return e;
     if (a.slots <= 8)
-      hipLaunchKernelGGL((k_attn_join<DC, 1, Shared>), dim3((unsigned)(rest.tiles * (rest.tile_rows / kWaves))), dim3(kThreads), 0,
-                         s, a);
+      hipLaunchKernelGGL(k_attn_join_few<DC>, dim3((unsigned)(rest.tiles * (rest.tile_rows / (kThreads / (16 * DC))))),
+                         dim3(kThreads), 0, s, a);
     else
       hipLaunchKernelGGL((k_attn_join<DC, kWaves, Shared>), dim3((unsigned)(rest.tiles * rest.tile_rows)), dim3(kThreads), 0, s, a);
     return hipGetLastError();
