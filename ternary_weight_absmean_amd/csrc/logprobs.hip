@@ -1,12 +1,14 @@
 // Log probabilities of given tokens, entropy and the most likely alternatives
 // (bl_logprobs), and their gradient (bl_logprobs_backward).
 //
-// With c = scale * log2 e, M = max x and d_j = (x_j - M) c:
+// With c = scale * log2 e, M = max x, B = fl(M c) and d_j = fma(x_j, c, -B):
 //   S = sum 2^d_j,  W = sum 2^d_j d_j,
-//   lse = scale M + ln S,  logprob_j = scale (x_j - M) - ln S,
 //   entropy = (log2 S - W / S) ln 2.
-// Differences are taken before the scale, so that rows of the type's lowest
-// value do not overflow.  All sums are fp32.
+// B's rounding is the same in every d, and known: delta = fma(M, c, -B).  With
+// log_s = (log2 S - delta) ln 2,
+//   lse = scale M + log_s,  logprob_j = scale (x_j - M) - log_s.
+// Where M c is not well inside fp32's range (rows of the type's lowest value),
+// d_j = (x_j - M) c instead.  All sums are fp32.
 //
 // A row is cut into chunks that one workgroup each holds in registers: one
 // reading of the logits gives the chunk's maximum, then (from the registers) S, W and
@@ -27,8 +29,6 @@ namespace {
 
 typedef unsigned v4u __attribute__((ext_vector_type(4)));
 
-constexpr int kThreads = 512;
-constexpr int kWaves = kThreads / 64;
 constexpr int kCandidates = 1024;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -0x1.fffffep127f;
@@ -103,11 +103,21 @@ __device__ __forceinline__ int wave_rth(int v, int r) {
   return top;
 }
 
+// What is taken off the exponents of a row or chunk whose maximum is top.
+struct Shift {
+  float b;
+  bool far;  // top * c near the end of fp32's range, or infinite
+  __device__ Shift(float top, float c) : b(top == -INFINITY ? 0.0f : top * c), far(!(fabsf(b) < 0x1p126f)) {}
+};
+
 struct Final {
   float top, scale, log_s, entropy, lse;
   // max, S and W of a whole row; S is 0 where nothing is possible
-  __device__ Final(const LogArgs& a, float most, float s, float w) : top(most), scale(a.scale), log_s(__log2f(s) * kLn2) {
-    entropy = s == 0.0f ? 0.0f : __builtin_fmaf(w / s, -kLn2, log_s);
+  __device__ Final(const LogArgs& a, float most, float s, float w) : top(most), scale(a.scale) {
+    const Shift shift(most, a.c);
+    const float log2_s = __log2f(s), delta = shift.far || most == -INFINITY ? 0.0f : __builtin_fmaf(most, a.c, -shift.b);
+    log_s = (log2_s - delta) * kLn2;
+    entropy = s == 0.0f ? 0.0f : (log2_s - w / s) * kLn2;
     lse = s == 0.0f ? -INFINITY : __builtin_fmaf(top, scale, log_s);
   }
   __device__ float logprob(float x) const {
@@ -138,8 +148,9 @@ __device__ __forceinline__ void rank_candidates(const uint64_t* place, int count
   }
 }
 
-template <bool kBf16, int E, bool kTop>
+template <bool kBf16, int E, bool kTop, int kThreads>
 __global__ __launch_bounds__(kThreads) void k_logprobs(LogArgs a) {
+  constexpr int kWaves = kThreads / 64;
   constexpr int kPer = Pieces<kBf16>::kPer;
   __shared__ float wave_top[kWaves], wave_s[kWaves], wave_w[kWaves];
   __shared__ int wave_limit[kWaves], counter[2];
@@ -190,21 +201,23 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogArgs a) {
     limit = fmaxf(value_of(max(least, order_of(-INFINITY))), kLowest);  // -infinity is no candidate
   }
 
-  const float most_finite = top == -INFINITY ? 0.0f : top;
+  const Shift shift(top, a.c);
   float s = 0.0f, w = 0.0f;
-  auto add = [&](float x) {
-    const float d = (x - most_finite) * a.c, e = __builtin_amdgcn_exp2f(d);
+  auto add_power = [&](float d) {
+    const float e = __builtin_amdgcn_exp2f(d);
     s += e;
     w = __builtin_fmaf(e, fmaxf(d, -300.0f), w);  // 0 * -infinity is 0 here
   };
-  // this thread's elements, each with its index
+  auto add = [&](float x) { add_power(__builtin_fmaf(x, a.c, -shift.b)); };
+  // This thread's elements, each with its index, read again: the rare passes
+  // over them take no registers from the first.
   auto each = [&](auto f) {
-    if (edge > -INFINITY) f(edge, (uint32_t)p.edge(tid));
+    if (chunk == 0 && tid < p.edges()) f(edge, (uint32_t)p.edge(tid));
+#pragma clang loop unroll(disable)
+    for (int v = v0 + tid; v < v1; v += kThreads) {
+      const v4u d = *p.vec(v);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const uint32_t first = (uint32_t)(p.head + (v0 + i * kThreads + tid) * kPer);
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) f(element<kBf16>(data[i], j), first + j);
+      for (int j = 0; j < kPer; ++j) f(element<kBf16>(d, j), (uint32_t)(p.head + v * kPer + j));
     }
   };
   auto collect = [&](float x, uint32_t index) {
@@ -215,6 +228,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogArgs a) {
   if (kTop && edge >= limit) collect(edge, (uint32_t)p.edge(tid));
 #pragma unroll
   for (int i = 0; i < E; ++i) {
+    asm("" : "+v"(data[i]));  // taken apart anew: elements kept from above would take twice the registers
 #pragma unroll
     for (int j = 0; j < kPer; ++j) add(element<kBf16>(data[i], j));
     if (kTop && most[i] >= limit) {
@@ -223,6 +237,11 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogArgs a) {
       for (int j = 0; j < kPer; ++j)
         if (element<kBf16>(data[i], j) >= limit) collect(element<kBf16>(data[i], j), first + j);
     }
+  }
+  asm("" : "+v"(s), "+v"(w));  // summed here, not behind the branch with all terms kept until there
+  if (shift.far) {
+    s = w = 0.0f;
+    each([&](float x, uint32_t) { add_power((x - top) * a.c); });
   }
   s = wave_sum(s);
   w = wave_sum(w);
@@ -296,30 +315,46 @@ __global__ __launch_bounds__(kJoinThreads) void k_logprobs_join(LogArgs a) {
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63;
   if (kTop && tid == 0) counter = 0;
+  // what is read goes out at once: the chunks' numbers, their alternatives (as
+  // many as four per thread), and in another wave the token's logit
+  const int held_best = kTop ? a.chunks * a.top : 0, r = kTop ? (a.top + a.chunks - 1) / a.chunks : 0;
+  const uint2* best = a.best + row * a.chunks * a.top;
+  uint2 ahead[kTop ? 4 : 1];
+  uint32_t rth = 0;
+  if (kTop) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ahead[i] = best[min(tid + i * kJoinThreads, held_best - 1)];
+    rth = best[min(lane, a.chunks - 1) * a.top + r - 1].y;
+  }
   float4 part = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
   if (lane < a.chunks) part = *reinterpret_cast<const float4*>(a.stats + 4 * (row * a.chunks + lane));
   const float top = value_of(wave_reduce<true>(order_of(part.x)));  // every wave has the row's
   // S and W relative to the row's maximum
-  const float shift = part.x == -INFINITY ? 0.0f : (part.x - top) * a.c;
+  const Shift whole(top, a.c);
+  const float shift = part.x == -INFINITY ? 0.0f : whole.far ? (part.x - top) * a.c : part.x * a.c - whole.b;
   const float e = __builtin_amdgcn_exp2f(shift);
   const float s = wave_sum(part.y * e), w = wave_sum(e * __builtin_fmaf(part.y, fmaxf(shift, -300.0f), part.z));
   const Final f(a, top, s, w);
-  if (tid == 0) store_row<kBf16>(a, row, f);
+  if (tid == kJoinThreads - 1) store_row<kBf16>(a, row, f);
   if (!kTop) return;
   // at least `top` are at or above the least of the chunks' r-th best
-  const int held = __float_as_int(part.w), r = (a.top + a.chunks - 1) / a.chunks;
+  const int held = __float_as_int(part.w);
   int limit = INT_MAX;
-  if (lane < a.chunks) {
-    limit = INT_MIN;
-    if (held >= r) limit = (int)(a.best[(row * a.chunks + lane) * a.top + r - 1].y ^ 0x80000000u);
-  }
+  if (lane < a.chunks) limit = held >= r ? (int)(rth ^ 0x80000000u) : INT_MIN;
   limit = -wave_reduce<true>(-max(limit, -INT_MAX));
   __syncthreads();
-  for (int i = tid; i < a.chunks * a.top; i += kJoinThreads) {
-    const int chunk = i / a.top, at = i - chunk * a.top;
-    if (at >= __float_as_int(a.stats[4 * (row * a.chunks + chunk) + 3])) continue;
-    const uint2 q = a.best[row * a.chunks * a.top + i];
-    if ((int)(q.y ^ 0x80000000u) >= limit) place[atomicAdd(&counter, 1)] = (uint64_t)q.y << 32 | q.x;
+  for (int base = 0; base < held_best; base += 4 * kJoinThreads) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = base + tid + i * kJoinThreads, chunk = min(k, held_best - 1) / a.top;
+      const int there = __shfl(held, chunk, 64);
+      if (k < held_best && k - chunk * a.top < there && (int)(ahead[i].y ^ 0x80000000u) >= limit)
+        place[atomicAdd(&counter, 1)] = (uint64_t)ahead[i].y << 32 | ahead[i].x;
+    }
+    if (base + 4 * kJoinThreads < held_best) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ahead[i] = best[min(base + 4 * kJoinThreads + tid + i * kJoinThreads, held_best - 1)];
+    }
   }
   __syncthreads();
   const int count = counter;
@@ -338,7 +373,10 @@ __global__ __launch_bounds__(kJoinThreads) void k_logprobs_join(LogArgs a) {
 // ---- gradient ----
 //   dx_j = scale * (g [j = t] + p_j (gz - g - gh (log p_j + H)))
 // with p_j = 2^d, d = fma(x_j, scale, -lse) log2 e.  Rows whose gradients are all
-// zero, and rows where nothing is possible, get zeros without being read.
+// zero, and rows where nothing is possible, get zeros without being read.  The
+// last rows come first: the forward call has left them in the Infinity Cache;
+// stores (and loads, which are the last of a row) go past the caches.  4096 x 128256
+// bf16, forward and this: 558 us, 605 in ascending order through the caches.
 struct GradArgs {
   const char* x;
   int64_t x_stride;
@@ -355,8 +393,9 @@ template <bool kBf16, int E, bool kAligned>
 __global__ __launch_bounds__(kGradThreads) void k_logprobs_backward(GradArgs a) {
   typedef Pieces<kBf16> P;
   constexpr int kPer = P::kPer;
-  const int64_t row = blockIdx.x / a.chunks;
-  const int chunk = (int)(blockIdx.x - row * a.chunks), tid = threadIdx.x;
+  const uint32_t block = gridDim.x - 1 - blockIdx.x;
+  const int64_t row = block / a.chunks;
+  const int chunk = (int)(block - row * a.chunks), tid = threadIdx.x;
   const P p(a.x, a.x_stride, row, a.n);
   const int per = (p.vecs + a.chunks - 1) / a.chunks, v0 = min(chunk * per, p.vecs), v1 = min(v0 + per, p.vecs);
   const int t = a.target ? a.target[row] : -1;
@@ -384,7 +423,7 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_backward(GradArgs a) 
   v4u data[E];
   if (!zero && v0 < v1) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) data[i] = *p.vec(min(v0 + i * kGradThreads + tid, v1 - 1));
+    for (int i = 0; i < E; ++i) data[i] = __builtin_nontemporal_load(p.vec(min(v0 + i * kGradThreads + tid, v1 - 1)));
   }
 #pragma unroll
   for (int i = 0; i < E; ++i) {
@@ -401,7 +440,7 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_backward(GradArgs a) 
       v4u w;
 #pragma unroll
       for (int j = 0; j < 4; ++j) w[j] = kBf16 ? f32x2_to_bf16x2(y[2 * j % kPer], y[(2 * j + 1) % kPer]) : __float_as_uint(y[j]);
-      *reinterpret_cast<v4u*>(out + (int64_t)first * P::kSize) = w;
+      __builtin_nontemporal_store(w, reinterpret_cast<v4u*>(out + (int64_t)first * P::kSize));
     } else {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) store(first + j, y[j]);
@@ -409,49 +448,56 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_backward(GradArgs a) 
   }
 }
 
-// Vectors of 16 bytes per thread: as many as registers hold (8) while the rows
-// still give the chip two workgroups per CU, fewer for few rows.
-// A row has never more chunks than the joining workgroup holds.
-int vectors_per_thread(int64_t m, int64_t n, int per) {
-  const int64_t vecs = (n + per - 1) / per;
-  auto chunks = [&](int e) { return (vecs + e * kThreads - 1) / (e * kThreads); };
-  int e = 8;
-  while (e > 1 && m * chunks(e) < 512 && chunks(e / 2) <= kMaxLogChunks) e >>= 1;
-  return e;
-}
-
+// One workgroup holds a row, in one launch, where the row has up to 4096 pieces
+// of 16 bytes (32768 bf16): 512 threads if rows are many, 1024 if few; for few
+// rows without alternatives up to 8192 (37 x 32003 fp32 6.3 us, 9.9 in chunks and
+// a join; 2000 x 60000 bf16 51 against 44).  Longer rows are cut into chunks of
+// eight pieces per thread while these still give the chip two workgroups per CU,
+// of fewer for few rows (64 x 128256 bf16 with alternatives: 15.4 us at 512
+// workgroups, 16.4 at 1024, 22.6 at 2048); never into more than the joining
+// workgroup holds.
 struct LogPlan {
-  int e;
+  int threads, e;
   int64_t chunks;
 };
-LogPlan log_plan(int64_t m, int64_t n, bool bf16) {
-  const int per = bf16 ? 8 : 4;
-  LogPlan p;
-  p.e = vectors_per_thread(m, n, per);
-  const int64_t vecs = (n + per - 1) / per, hold = (int64_t)p.e * kThreads;
-  p.chunks = (vecs + hold - 1) / hold;
-  return p;
+LogPlan log_plan(int64_t m, int64_t n, bool bf16, bool top) {
+  const int64_t vecs = bf16 ? (n + 7) / 8 : (n + 3) / 4;
+  if (vecs <= 4096 || (vecs <= 8192 && m < 512 && !top)) {
+    const int threads = vecs <= 512 || (m >= 512 && vecs <= 4096) ? 512 : 1024;
+    int e = 1;
+    while (e * threads < vecs) e <<= 1;
+    return {threads, e, 1};
+  }
+  auto chunks = [&](int e) { return (vecs + e * 512 - 1) / (e * 512); };
+  int e = 8;
+  while (e > 1 && m * chunks(e) < 512 && chunks(e / 2) <= kMaxLogChunks) e >>= 1;
+  return {512, e, chunks(e)};
 }
 
 }  // namespace
 
 size_t logprobs_workspace_bytes(int64_t m, int64_t n, bool bf16, int64_t top) {
-  const LogPlan p = log_plan(m, n, bf16);
+  const LogPlan p = log_plan(m, n, bf16, top > 0);
   return p.chunks == 1 ? 0 : (size_t)(m * p.chunks) * (16 + 8 * (size_t)top);
 }
 
 hipError_t launch_logprobs(const void* x, bool bf16, int64_t m, int64_t n, int64_t stride, float scale,
                            const int32_t* target, int64_t top, float* logprob, float* lse, float* entropy, int32_t* top_id,
                            float* top_logprob, void* workspace, hipStream_t s) {
-  const LogPlan p = log_plan(m, n, bf16);
-  if (!grid_fits(m * p.chunks, kThreads)) return kErrGridTooLarge;
+  const LogPlan p = log_plan(m, n, bf16, top > 0);
+  if (!grid_fits(m * p.chunks, p.threads)) return kErrGridTooLarge;
   LogArgs a = {(const char*)x, stride * (bf16 ? 2 : 4), (int)n,      (int)p.chunks, (int)top, scale, scale * kLog2e,
                target,         logprob,                 lse,     entropy,       top_id,   top_logprob};
   a.stats = (float*)workspace;
   a.best = (uint2*)(a.stats + 4 * m * p.chunks);
-  auto go = [&](auto b, auto e, auto with_top) {
+  const dim3 grid((unsigned)(m * p.chunks));
+  auto go = [&](auto b, auto with_top, auto e) {
     constexpr bool kBf16 = decltype(b)::value, kTop = decltype(with_top)::value;
-    hipLaunchKernelGGL((k_logprobs<kBf16, decltype(e)::value, kTop>), dim3((unsigned)(m * p.chunks)), dim3(kThreads), 0, s, a);
+    constexpr int E = decltype(e)::value;
+    if (p.threads == 1024)
+      hipLaunchKernelGGL((k_logprobs<kBf16, E, kTop, 1024>), grid, dim3(1024), 0, s, a);
+    else
+      hipLaunchKernelGGL((k_logprobs<kBf16, E, kTop, 512>), grid, dim3(512), 0, s, a);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || p.chunks == 1) return err;
     hipLaunchKernelGGL((k_logprobs_join<kBf16, kTop>), dim3((unsigned)m), dim3(kJoinThreads), 0, s, a);
@@ -461,10 +507,10 @@ hipError_t launch_logprobs(const void* x, bool bf16, int64_t m, int64_t n, int64
   using std::integral_constant;
   auto by_e = [&](auto b, auto with_top) {
     switch (p.e) {
-      case 1: return go(b, integral_constant<int, 1>{}, with_top);
-      case 2: return go(b, integral_constant<int, 2>{}, with_top);
-      case 4: return go(b, integral_constant<int, 4>{}, with_top);
-      default: return go(b, integral_constant<int, 8>{}, with_top);
+      case 1: return go(b, with_top, integral_constant<int, 1>{});
+      case 2: return go(b, with_top, integral_constant<int, 2>{});
+      case 4: return go(b, with_top, integral_constant<int, 4>{});
+      default: return go(b, with_top, integral_constant<int, 8>{});
     }
   };
   auto by_top = [&](auto b) { return top > 0 ? by_e(b, bool_constant<true>{}) : by_e(b, bool_constant<false>{}); };
