@@ -173,12 +173,15 @@ __global__ __launch_bounds__(kThreads) void k_kv_grow(Grow g) {
 }
 
 // ---- bl_kv_fork ----
+constexpr int64_t kReleaseHere = 32768;
+
 struct Fork {
   int32_t* refs;
   int pages, page_tokens;
   const int32_t *table, *length, *parent;
   int64_t stride;
   int seqs, children, keep_parents;
+  bool release_here;  // workgroup 0 also gives back what no child holds
   int32_t *table_out, *length_out, *copies, *shortage;
   __device__ bool parent_of(int c, int& p) const {
     p = parent[c];
@@ -264,10 +267,18 @@ __global__ __launch_bounds__(kThreads) void k_kv_fork(Fork f) {
   };
   const int lacking = hand_out(f.refs, f.pages, f.children, queue, part, need, give);
   if (tid == 0 && f.shortage && lacking > 0) *f.shortage += lacking;
+  if (!f.release_here) return;
+  for (int i = tid; i < f.seqs * (int)f.stride; i += kThreads) {
+    const int p = i / (int)f.stride, at = i - p * (int)f.stride;
+    const int64_t from = first[p] < f.children ? (f.held(p) + f.page_tokens - 1) / f.page_tokens : 0;
+    if (at >= from) release(f.refs, f.pages, f.table[i]);
+  }
 }
 
 // The pages of consumed parents that no child took over: all of a parent without
-// children, those past the length of the others.
+// children, those past the length of the others.  Each is one of the parent's own
+// holds, so no count falls to 0 while another row's workgroup raises it.  In a
+// launch of its own where the rows are long (kReleaseHere entries and more).
 __global__ __launch_bounds__(256) void k_kv_fork_release(Fork f) {
   const int p = (int)blockIdx.x, tid = threadIdx.x;
   bool has = false;
@@ -297,13 +308,15 @@ __global__ __launch_bounds__(256) void k_kv_free(int32_t* refs, int pages, int p
 // over the blocks before, taken by every block itself; lists, counts, tables.
 constexpr int kCountThreads = 256;
 constexpr int kBlockPages = 4096;
+constexpr int kOnePages = 16 * kThreads;  // pool of k_kv_compact
+constexpr int64_t kOneEntries = 32768;    // and its tables' entries
 
 struct Compact {
   int32_t* refs;
   int pages, page_tokens;
   int32_t* table;
   int64_t entries;
-  int moves;
+  int moves, asked;  // asked: entries of copies
   int32_t *copies, *moved;
   int32_t *counts, *above, *source, *target, *rank;  // workspace: per block, one, per move (two), per page
 };
@@ -352,6 +365,47 @@ __device__ __forceinline__ void sums_of(const int32_t* counts, int blocks, int b
   before = part[4] + part[5] + part[6] + part[7];
 }
 
+// The ranks of 16 pages from `first` on, `used` used ones before them, of n in all.
+__device__ __forceinline__ void rank_pages(const Compact& c, int first, int bits, int used, int n) {
+  for (int j = 0; j < 16 && first + j < c.pages; ++j) {
+    const int p = first + j;
+    const bool in_use = bits >> j & 1;
+    if (p == n) *c.above = n - used;  // used pages from n on: as many as free ones below
+    if (p < n) {
+      if (!in_use && p - used < c.moves) c.target[p - used] = p;
+    } else {
+      const int r = in_use ? n - 1 - used : -1;
+      c.rank[p] = r;
+      if (in_use && r < c.moves) c.source[r] = p;
+    }
+    used += in_use;
+  }
+}
+
+__device__ __forceinline__ void no_copy(const Compact& c, int64_t i) {
+  c.copies[3 * i] = c.copies[3 * i + 1] = -1;
+  c.copies[3 * i + 2] = 0;
+}
+
+// Item i: a move, or behind them an entry of the tables.
+__device__ __forceinline__ void rename(const Compact& c, int64_t i, int n, int moved) {
+  if (i >= c.moves) {
+    const int32_t e = c.table[i - c.moves];
+    if (e < n || e >= c.pages) return;
+    const int r = c.rank[e];
+    if (r >= 0 && r < moved) c.table[i - c.moves] = c.target[r];
+  } else if (i < moved) {
+    const int from = c.source[i], to = c.target[i];
+    c.copies[3 * i] = from;
+    c.copies[3 * i + 1] = to;
+    c.copies[3 * i + 2] = c.page_tokens;
+    c.refs[to] = c.refs[from];
+    c.refs[from] = 0;
+  } else {
+    no_copy(c, i);
+  }
+}
+
 __global__ __launch_bounds__(kCountThreads) void k_kv_rank(Compact c) {
   __shared__ int part[8], wave_used[4];
   const int blocks = (int)gridDim.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -370,48 +424,43 @@ __global__ __launch_bounds__(kCountThreads) void k_kv_rank(Compact c) {
   for (int w = 0; w < wave; ++w) used += wave_used[w];
   used += sum - mine;  // used pages before this thread's first
   if (blockIdx.x == 0 && tid == 0 && n == c.pages) *c.above = 0;
-  for (int j = 0; j < 16 && first + j < c.pages; ++j) {
-    const int p = first + j;
-    const bool in_use = bits >> j & 1;
-    if (p == n) *c.above = n - used;  // used pages from n on: as many as free ones below
-    if (p < n) {
-      if (!in_use && p - used < c.moves) c.target[p - used] = p;
-    } else {
-      const int r = in_use ? n - 1 - used : -1;
-      c.rank[p] = r;
-      if (in_use && r < c.moves) c.source[r] = p;
-    }
-    used += in_use;
-  }
+  rank_pages(c, first, bits, used, n);
 }
 
-__global__ __launch_bounds__(kCountThreads) void k_kv_rename(Compact c, int blocks, int64_t items) {
+__global__ __launch_bounds__(kCountThreads) void k_kv_rename(Compact c, int blocks) {
   __shared__ int part[8];
   int before, n;
   sums_of(c.counts, blocks, 0, part, before, n);
   const int moved = min(*c.above, c.moves);
   if (blockIdx.x == 0 && threadIdx.x == 0) *c.moved = moved;
-  for (int64_t i = (int64_t)blockIdx.x * kCountThreads + threadIdx.x; i < items; i += (int64_t)gridDim.x * kCountThreads) {
-    if (i < c.moves) {
-      int32_t* copy = c.copies + 3 * i;
-      if (i < moved) {
-        const int from = c.source[i], to = c.target[i];
-        copy[0] = from;
-        copy[1] = to;
-        copy[2] = c.page_tokens;
-        c.refs[to] = c.refs[from];
-        c.refs[from] = 0;
-      } else {
-        copy[0] = copy[1] = -1;
-        copy[2] = 0;
-      }
-    } else {
-      const int32_t e = c.table[i - c.moves];
-      if (e < n || e >= c.pages) continue;
-      const int r = c.rank[e];
-      if (r >= 0 && r < moved) c.table[i - c.moves] = c.target[r];
-    }
-  }
+  for (int64_t i = (int64_t)blockIdx.x * kCountThreads + threadIdx.x; i < c.moves + c.entries;
+       i += (int64_t)gridDim.x * kCountThreads)
+    rename(c, i, n, moved);
+}
+
+// All of it in one workgroup with its lists in LDS, for a pool and tables that
+// it is done with sooner than three launches are (2048 pages, 1536 entries: 5 us
+// against 12).
+__global__ __launch_bounds__(kThreads) void k_kv_compact(Compact c) {
+  __shared__ int part[kThreads / 64], above;
+  __shared__ int rank[kOnePages], target[kOnePages / 2], source[kOnePages / 2];
+  const int tid = threadIdx.x, first = 16 * tid;
+  const int bits = used_bits(c.refs, first, c.pages);
+  int n;
+  const int used = block_prefix(__popc(bits), part, n);
+  c.above = &above;
+  c.rank = rank;
+  c.target = target;
+  c.source = source;
+  if (tid == 0 && n == c.pages) above = 0;
+  // no more of them than there are used pages above n, or free ones below
+  c.moves = min(c.moves, kOnePages / 2);
+  rank_pages(c, first, bits, used, n);
+  __syncthreads();
+  const int moved = min(above, c.moves);
+  if (tid == 0) *c.moved = moved;
+  for (int64_t i = tid; i < c.moves + c.entries; i += kThreads) rename(c, i, n, moved);
+  for (int64_t i = c.moves + tid; i < c.asked; i += kThreads) no_copy(c, i);
 }
 
 // ---- bl_kv_copy ----
@@ -487,14 +536,15 @@ hipError_t launch_kv_grow(int32_t* refs, int64_t pages, int page_tokens, const K
 hipError_t launch_kv_fork(int32_t* refs, int64_t pages, int page_tokens, const int32_t* table, int64_t stride,
                           const int32_t* length, int64_t seqs, const int32_t* parent, int64_t children, bool keep_parents,
                           int32_t* table_out, int32_t* length_out, int32_t* copies, int32_t* shortage, hipStream_t s) {
-  const Fork f = {refs,   (int)pages, page_tokens,   table,      length, parent,  stride, (int)seqs,
-                  (int)children, keep_parents, table_out, length_out, copies, shortage};
+  const bool here = !keep_parents && children > 0 && seqs * stride <= kReleaseHere;
+  const Fork f = {refs,          (int)pages,   page_tokens, table,     length,     parent, stride,  (int)seqs,
+                  (int)children, keep_parents, here,        table_out, length_out, copies, shortage};
   if (children > 0) {
     hipLaunchKernelGGL(k_kv_fork, dim3(1 + (unsigned)children), dim3(kThreads), 0, s, f);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (keep_parents || seqs == 0) return hipSuccess;
+  if (keep_parents || seqs == 0 || here) return hipSuccess;
   hipLaunchKernelGGL(k_kv_fork_release, dim3((unsigned)seqs), dim3(256), 0, s, f);
   return hipGetLastError();
 }
@@ -512,7 +562,11 @@ size_t kv_compact_workspace_bytes(int64_t pages, int64_t moves) {
 hipError_t launch_kv_compact(int32_t* refs, int64_t pages, int page_tokens, int32_t* table, int64_t stride, int64_t seqs,
                              int64_t moves, int32_t* copies, int32_t* moved, void* workspace, hipStream_t s) {
   const int64_t blocks = compact_blocks(pages), entries = seqs * stride;
-  Compact c = {refs, (int)pages, page_tokens, table, entries, (int)moves, copies, moved};
+  Compact c = {refs, (int)pages, page_tokens, table, entries, (int)moves, (int)moves, copies, moved};
+  if (pages <= kOnePages && entries <= kOneEntries) {
+    hipLaunchKernelGGL(k_kv_compact, dim3(1), dim3(kThreads), 0, s, c);
+    return hipGetLastError();
+  }
   c.counts = (int32_t*)workspace;
   c.above = c.counts + blocks;
   c.source = c.above + 1;
@@ -524,9 +578,9 @@ hipError_t launch_kv_compact(int32_t* refs, int64_t pages, int page_tokens, int3
   hipLaunchKernelGGL(k_kv_rank, dim3((unsigned)blocks), dim3(kCountThreads), 0, s, c);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t items = moves + entries, wanted = (items + kCountThreads - 1) / kCountThreads;
+  const int64_t wanted = (moves + entries + kCountThreads - 1) / kCountThreads;
   hipLaunchKernelGGL(k_kv_rename, dim3((unsigned)(wanted < 1 ? 1 : wanted < 2048 ? wanted : 2048)), dim3(kCountThreads), 0, s,
-                     c, (int)blocks, items);
+                     c, (int)blocks);
   return hipGetLastError();
 }
 

@@ -200,6 +200,15 @@ def test_forking_at_the_largest():
     b.fork(lengths, rng.integers(seqs, size=8192).tolist(), False)
 
 
+def test_forking_wide_tables():
+    """Rows so long that consumed parents' pages are given back by a launch of its own."""
+    rng = np.random.default_rng(4)
+    lengths = [16 * 9000 + 5, 40, 16 * 11000, 7, 0]
+    b = Both(30000, 16, scattered(rng, 30000, 16, lengths, 12000))
+    say("bl_kv_fork wide")
+    b.fork([16 * 9000 + 5, 17, 16 * 10500, 7, 0], [2, 0, 0, 1, 4], False)
+
+
 def test_freeing():
     rng = np.random.default_rng(8)
     lengths = [0, 5, 16, 17, 160, 100]
