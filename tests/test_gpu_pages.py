@@ -140,6 +140,18 @@ def test_shared_pages_are_copied_before_they_are_written(free):
         assert b.model.refs[5] == 1 and b.model.refs[9] == 1 and b.model_short == 0
 
 
+@pytest.mark.parametrize("pages,free", [(70000, [69999]), (200000, [8191, 8192, 65536, 131071, 199999]), (1 << 18, [150000, 150001]),
+                                        (150001, [])])
+def test_free_pages_far_behind_used_ones(pages, free):
+    refs = np.ones(pages, int)
+    refs[free] = 0
+    b = Both(pages, 16, [[-1], [-1], [-1], [-1]], refs.tolist())
+    say(f"bl_kv_grow far pages={pages}")
+    b.grow([0, 0, 0, 0], [1, 1, 1, 1])
+    b.free([1, 0, 0, 1])
+    b.grow([0, 0, 0, 0], [1, 1, 1, 1])
+
+
 def test_growing_with_odd_integers():
     """Positions before 0, past the table, offsets that do not ascend: what the header says of them."""
     b = Both(50, 16, [[-1, -1, -1], [-1, 60, -7], [3, -1, -1]])
