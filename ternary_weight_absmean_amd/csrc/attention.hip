@@ -1266,7 +1266,16 @@ struct SharedPlan {
   int64_t slots() const { return pre.splits + (finish && rest.splits == 1 ? 0 : rest.splits); }
 };
 
-constexpr int64_t kSharedBlocks = 512;
+// Workgroups in all: two per CU of the kernel for many rows, one of that for few
+// (a decode step of 12 answers of 64/8 heads to 8192 tokens: 21 us at 256, 25 at
+// 512, 32 at 128), so that most rows have few partial sums to join and a rest of
+// one split needs no join at all (32 answers: 35 us, 45 with two).
+constexpr int64_t kSharedBlocks = 512, kSharedFew = 256;
+// The prefixes' rows go to the kernel for few rows while its tiles times their
+// steps of 64 elements are few: 16 answers as above (16384) 23 us against 41, but
+// four such groups of 12 (49152) 67 against 43; at 32768 either may win (32 answers
+// 36 against 35, 4 x 8 43 against 39).
+constexpr int64_t kFewWork = 32768;
 
 SharedPlan make_shared_plan(const KvView& kv, int64_t tokens, int64_t max_new, int64_t max_len, int64_t q_heads,
                             int64_t groups, int64_t max_group, int64_t max_prefix) {
@@ -1282,15 +1291,20 @@ SharedPlan make_shared_plan(const KvView& kv, int64_t tokens, int64_t max_new, i
   rest.row_tiles = (rows + rest.tile_rows - 1) / rest.tile_rows;
   rest.tiles = lists * rest.row_tiles;
   const int64_t most = max_group * max_new < tokens ? max_group * max_new : tokens;
-  pre.tile_rows = most * group < 64 ? 16 : kPromptRows;
+  const int64_t few = groups * kv.heads * ((most * group + 15) / 16), chunks = kv.dim <= 64 ? 1 : 2;
+  pre.tile_rows = few * pre_steps * chunks < kFewWork ? 16 : kPromptRows;
   pre.row_tiles = (most * group + pre.tile_rows - 1) / pre.tile_rows;
   pre.tiles = groups * kv.heads * pre.row_tiles;
   p.finish = rest.tile_rows == 16 && (pre.tile_rows != 16 || pre_steps == 0);
   const int64_t all = p.finish ? pre.tiles : pre.tiles + rest.tiles;
   pre.teams = pre.tile_rows != 16 && kv.dim <= 128 && all < 256 ? 2 : 1;
   rest.teams = rest.tile_rows != 16 ? pre.teams : 1;
-  rest.splits = pick(rest.tiles, kSharedBlocks / rest.teams, steps, kWaves);
-  pre.splits = pick(pre.tiles, kSharedBlocks / pre.teams, pre_steps, kWaves);
+  // Four splits stay for sequences that share little and are long.  As many as
+  // fit in max_len would cost 6 us more where their sums then take the other join.
+  const int64_t likely = steps - pre_steps > 4 * kWaves ? steps - pre_steps : 4 * kWaves;
+  rest.splits = pick(rest.tiles, rest.tile_rows == 16 ? kSharedFew : kSharedBlocks / rest.teams, steps < likely ? steps : likely,
+                     kWaves);
+  pre.splits = pick(pre.tiles, pre.tile_rows == 16 ? kSharedFew : kSharedBlocks / pre.teams, pre_steps, kWaves);
   pre.per = rest.per = kWaves;
   return p;
 }
