@@ -86,15 +86,24 @@ __device__ __forceinline__ uint64_t place_of(float value, uint32_t index) {
   return (uint64_t)((uint32_t)order_of(value) ^ 0x80000000u) << 32 | (0xFFFFFFFFu - index);
 }
 
+// Sum over a wave, the same in every lane: lane moves inside rows of 16 (as in
+// lane_group_reduce), then the rows' sums.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
-  return v;
+  auto moved = [&](auto control) {
+    const int b = __float_as_int(v);
+    v += __int_as_float(__builtin_amdgcn_update_dpp(b, b, decltype(control)::value, 0xF, 0xF, false));
+  };
+  moved(std::integral_constant<int, 0xB1>{});
+  moved(std::integral_constant<int, 0x4E>{});
+  moved(std::integral_constant<int, 0x141>{});
+  moved(std::integral_constant<int, 0x140>{});
+  auto row = [&](int lane) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane)); };
+  return (row(0) + row(16)) + (row(32) + row(48));
 }
 
-// The r-th largest of the lanes' values (as order_of), INT_MIN if there is none.
-__device__ __forceinline__ int wave_rth(int v, int r) {
-  int top = wave_reduce<true>(v);
+// The r-th largest of the lanes' values (as order_of), the largest being top;
+// INT_MIN if there is none.
+__device__ __forceinline__ int wave_rth(int v, int top, int r) {
   for (int i = 1; i < r; ++i) {
     const uint64_t at = __ballot(v == top);
     if ((int)(threadIdx.x & 63) == __ffsll((unsigned long long)at) - 1) v = INT_MIN;
@@ -187,7 +196,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogArgs a) {
   if (lane == 0) wave_top[wave] = value_of(wave_key);
   const int full = max(min((v1 - v0) / 64, kWaves), 1);  // waves with an element in every lane
   if (kTop) {
-    const int limit = wave_rth(key, (a.top + full - 1) / full);
+    const int limit = wave_rth(key, wave_key, (a.top + full - 1) / full);
     if (lane == 0) wave_limit[wave] = limit;
   }
   __syncthreads();
@@ -225,17 +234,35 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogArgs a) {
     if (at < kCandidates) place[at] = place_of(x, index);
   };
   add(edge);
-  if (kTop && edge >= limit) collect(edge, (uint32_t)p.edge(tid));
+  int hits = 0;  // pieces with candidates
 #pragma unroll
   for (int i = 0; i < E; ++i) {
     asm("" : "+v"(data[i]));  // taken apart anew: elements kept from above would take twice the registers
 #pragma unroll
     for (int j = 0; j < kPer; ++j) add(element<kBf16>(data[i], j));
-    if (kTop && most[i] >= limit) {
-      const uint32_t first = (uint32_t)(p.head + (v0 + i * kThreads + tid) * kPer);
+    if (kTop) hits |= (most[i] >= limit) << i;
+  }
+  if (kTop) {
+    // Few lanes have one, and one as a rule: loops, since code that is not in the
+    // instruction cache costs more (unrolled, one row of 128256 bf16 took 1 us more).
+    if (edge >= limit) collect(edge, (uint32_t)p.edge(tid));
+    while (hits) {
+      const int i = __ffs(hits) - 1;
+      hits &= hits - 1;
+      v4u d = data[0];
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (element<kBf16>(data[i], j) >= limit) collect(element<kBf16>(data[i], j), first + j);
+      for (int k = 1; k < E; ++k)
+        if (k == i) d = data[k];
+      int bits = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) bits |= (element<kBf16>(d, j) >= limit) << j;
+      while (bits) {
+        const int j = __ffs(bits) - 1, word = kBf16 ? j >> 1 : j;
+        bits &= bits - 1;
+        const uint32_t w = word & 2 ? (word & 1 ? d[3] : d[2]) : (word & 1 ? d[1] : d[0]);
+        const float x = __uint_as_float(!kBf16 ? w : j & 1 ? w & 0xFFFF0000u : w << 16);
+        collect(x, (uint32_t)(p.head + (v0 + i * kThreads + tid) * kPer + j));
+      }
     }
   }
   asm("" : "+v"(s), "+v"(w));  // summed here, not behind the branch with all terms kept until there
@@ -317,7 +344,8 @@ __global__ __launch_bounds__(kJoinThreads) void k_logprobs_join(LogArgs a) {
   if (kTop && tid == 0) counter = 0;
   // what is read goes out at once: the chunks' numbers, their alternatives (as
   // many as four per thread), and in another wave the token's logit
-  const int held_best = kTop ? a.chunks * a.top : 0, r = kTop ? (a.top + a.chunks - 1) / a.chunks : 0;
+  const int held_best = kTop ? a.chunks * a.top : 0;
+  const int of_chunks = min(a.chunks, 8), r = (a.top + of_chunks - 1) / of_chunks;
   const uint2* best = a.best + row * a.chunks * a.top;
   uint2 ahead[kTop ? 4 : 1];
   uint32_t rth = 0;
@@ -337,11 +365,11 @@ __global__ __launch_bounds__(kJoinThreads) void k_logprobs_join(LogArgs a) {
   const Final f(a, top, s, w);
   if (tid == kJoinThreads - 1) store_row<kBf16>(a, row, f);
   if (!kTop) return;
-  // at least `top` are at or above the least of the chunks' r-th best
+  // at least `top` are at or above the eighth largest (the least, of fewer) of the
+  // chunks' r-th best
   const int held = __float_as_int(part.w);
-  int limit = INT_MAX;
-  if (lane < a.chunks) limit = held >= r ? (int)(rth ^ 0x80000000u) : INT_MIN;
-  limit = -wave_reduce<true>(-max(limit, -INT_MAX));
+  int limit = lane < a.chunks && held >= r ? (int)(rth ^ 0x80000000u) : INT_MIN;
+  limit = wave_rth(limit, wave_reduce<true>(limit), of_chunks);
   __syncthreads();
   for (int base = 0; base < held_best; base += 4 * kJoinThreads) {
 #pragma unroll
