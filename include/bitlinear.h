@@ -525,8 +525,11 @@ typedef struct bl_kv_pool {
  *           {-1, -1, 0} elsewhere; of sequences of the batch that share it, the
  *           last one keeps it if nobody else does.  Such pages come from
  *           cutting back (bl_kv_free with keep) into pages that a fork shares.
+ *           Where no page was free for a copy the entry stays as it is, shared:
+ *           such a sequence must not be written.
  * Errors: BL_ERR_NULL, BL_ERR_SHAPE (also when sequences times the pages that
- * max_new tokens may enter pass 2^24), BL_ERR_ALIGN, BL_ERR_HIP. */
+ * max_new tokens may enter pass 2^24, or seqs passes BL_MAX_FORK_SEQS with
+ * copies), BL_ERR_ALIGN, BL_ERR_HIP. */
 bl_status bl_kv_grow(const bl_kv_pool* pool, const bl_kv_batch* batch, int32_t* copies, int32_t* shortage, void* stream);
 
 /* Forks sequences: child c continues parent p = parent[c], which holds
@@ -592,8 +595,9 @@ bl_status bl_kv_copy(const bl_kv_cache* caches, int64_t count, const int32_t* co
  * others' entries for them need not name the same pages, if theirs hold the
  * same tokens).  No prefix[g] passes the start of one of its sequences.
  * max_group bounds group[g + 1] - group[g], max_prefix the prefixes.  Values
- * that break these bounds give no error and no access outside a buffer: they
- * are taken as inside them; sequences in no group are left out. */
+ * that break these bounds, or those of bl_kv_batch, give no error and no access
+ * outside a buffer; the outputs of their group mean nothing then.  Sequences in
+ * no group are left out, their outputs as they were. */
 typedef struct bl_kv_shared {
     const int32_t* group;  /* device [groups + 1], ascending from 0 to seqs */
     const int32_t* prefix; /* device [groups]                               */

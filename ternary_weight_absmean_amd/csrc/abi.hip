@@ -457,7 +457,7 @@ bl_status check_shared(const bl_kv_cache* cache, const bl_kv_batch* batch, const
       shared->max_prefix < 0 || shared->max_prefix > batch->max_len || shared->groups * shared->max_group < batch->seqs ||
       !q_heads_ok(q_heads) || q_heads % cache->heads != 0 ||
       shared->groups * shared->max_group > kMaxPositions / cache->heads ||
-      batch->tokens * (q_heads / cache->heads) > kMaxPositions)
+      batch->tokens * (q_heads / cache->heads) > kMaxPositions || !product_ok(batch->tokens, q_heads * cache->dim))
     return BL_ERR_SHAPE;
   return BL_OK;
 }
@@ -511,7 +511,8 @@ bl_status bl_kv_grow(const bl_kv_pool* pool, const bl_kv_batch* batch, int32_t* 
   if (bl_status st = check_pool(pool, batch->seqs, batch->table_stride)) return st;
   if (batch->tokens < 0 || batch->tokens > kMaxPositions || batch->max_new < 0 || batch->max_new > batch->tokens ||
       batch->max_len < batch->max_new || batch->max_len > batch->table_stride * pool->page_tokens ||
-      batch->seqs * ((batch->max_new + pool->page_tokens - 2) / pool->page_tokens + 1) > bl::kMaxGrowItems)
+      batch->seqs * ((batch->max_new + pool->page_tokens - 2) / pool->page_tokens + 1) > bl::kMaxGrowItems ||
+      (copies && batch->seqs > BL_MAX_FORK_SEQS))
     return BL_ERR_SHAPE;
   if (nothing_new(batch)) return BL_OK;  // empty tensors may carry NULL pointers
   if (!pool->refs || !batch->page_table || !batch->start || !batch->offsets) return BL_ERR_NULL;

@@ -1292,7 +1292,7 @@ SharedPlan make_shared_plan(const KvView& kv, int64_t tokens, int64_t max_new, i
   rest.tiles = lists * rest.row_tiles;
   const int64_t most = max_group * max_new < tokens ? max_group * max_new : tokens;
   const int64_t few = groups * kv.heads * ((most * group + 15) / 16), chunks = kv.dim <= 64 ? 1 : 2;
-  pre.tile_rows = few * pre_steps * chunks < kFewWork ? 16 : kPromptRows;
+  pre.tile_rows = few < kFewWork && few * pre_steps * chunks < kFewWork ? 16 : kPromptRows;
   pre.row_tiles = (most * group + pre.tile_rows - 1) / pre.tile_rows;
   pre.tiles = groups * kv.heads * pre.row_tiles;
   p.finish = rest.tile_rows == 16 && (pre.tile_rows != 16 || pre_steps == 0);

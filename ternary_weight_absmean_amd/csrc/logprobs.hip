@@ -478,19 +478,19 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_backward(GradArgs a) 
 
 // One workgroup holds a row, in one launch, where the row has up to 4096 pieces
 // of 16 bytes (32768 bf16): 512 threads if rows are many, 1024 if few; for few
-// rows without alternatives up to 8192 (37 x 32003 fp32 6.3 us, 9.9 in chunks and
-// a join; 2000 x 60000 bf16 51 against 44).  Longer rows are cut into chunks of
-// eight pieces per thread while these still give the chip two workgroups per CU,
-// of fewer for few rows (64 x 128256 bf16 with alternatives: 15.4 us at 512
-// workgroups, 16.4 at 1024, 22.6 at 2048); never into more than the joining
-// workgroup holds.
+// rows up to 8192 (37 x 32003 fp32 6.6 us, 9.5 in chunks and a join; 2000 x 60000
+// bf16 51 against 43; with alternatives 1 x 65000 9.1 against 10.1, but 333 x 30000
+// fp32 15.7 against 14.6).  Longer rows are cut into chunks of eight pieces per
+// thread while these still make a workgroup per CU, of fewer for few rows (64 x
+// 128256 bf16 with 20 alternatives: 12.7 us at 256 workgroups, 13.4 at 512, 14.6 at
+// 1024, 19 at 2048); never into more than the joining workgroup holds.
 struct LogPlan {
   int threads, e;
   int64_t chunks;
 };
 LogPlan log_plan(int64_t m, int64_t n, bool bf16, bool top) {
   const int64_t vecs = bf16 ? (n + 7) / 8 : (n + 3) / 4;
-  if (vecs <= 4096 || (vecs <= 8192 && m < 512 && !top)) {
+  if (vecs <= 4096 || (vecs <= 8192 && m < (top ? 32 : 512))) {
     const int threads = vecs <= 512 || (m >= 512 && vecs <= 4096) ? 512 : 1024;
     int e = 1;
     while (e * threads < vecs) e <<= 1;
@@ -498,7 +498,7 @@ LogPlan log_plan(int64_t m, int64_t n, bool bf16, bool top) {
   }
   auto chunks = [&](int e) { return (vecs + e * 512 - 1) / (e * 512); };
   int e = 8;
-  while (e > 1 && m * chunks(e) < 512 && chunks(e / 2) <= kMaxLogChunks) e >>= 1;
+  while (e > 1 && m * chunks(e) < 256 && chunks(e / 2) <= kMaxLogChunks) e >>= 1;
   return {512, e, chunks(e)};
 }
 

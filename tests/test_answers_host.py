@@ -37,7 +37,8 @@ def test_kv_grow_refusals():
     check_pool(call)
     for bad in (dict(seqs=-1), dict(seqs=65536), dict(tokens=-1), dict(max_new=-1), dict(max_new=7), dict(max_len=2),
                 dict(max_len=65), dict(stride=-1), dict(stride=1 << 26), dict(tokens=(1 << 29) + 1),
-                dict(seqs=60000, tokens=1 << 14, max_new=1 << 14, max_len=1 << 14, stride=1 << 10)):
+                dict(seqs=60000, tokens=1 << 14, max_new=1 << 14, max_len=1 << 14, stride=1 << 10),
+                dict(seqs=8193, copies=FAKE)):
         assert call(**bad) == BL_ERR_SHAPE, bad
     for name in ("table", "start", "offsets"):
         assert call(**{name: None}) == BL_ERR_NULL
@@ -139,6 +140,7 @@ def test_attention_shared_refusals():
     assert lib.bl_attention_shared(cp, bp, None, FAKE, 256, 64, 4, 0.125, FAKE, None, FAKE, 1 << 40, None) == BL_ERR_NULL
     for bad in (dict(groups=1), dict(groups=-1), dict(max_group=0), dict(max_group=-1), dict(groups=65536), dict(max_group=65536),
                 dict(max_prefix=-1), dict(max_prefix=41), dict(q_heads=3), dict(q_heads=0), dict(scale=math.nan),
+                dict(heads=65536, q_heads=65536, tokens=1 << 18, max_new=1, max_len=64),
                 dict(scale=math.inf)):
         assert call(**bad) == BL_ERR_SHAPE, bad
     for name in ("q", "out", "ws", "group", "prefix"):
