@@ -596,8 +596,8 @@ bl_status bl_kv_copy(const bl_kv_cache* caches, int64_t count, const int32_t* co
  * same tokens).  No prefix[g] passes the start of one of its sequences.
  * max_group bounds group[g + 1] - group[g], max_prefix the prefixes.  Values
  * that break these bounds, or those of bl_kv_batch, give no error and no access
- * outside a buffer; the outputs of their group mean nothing then.  Sequences in
- * no group are left out, their outputs as they were. */
+ * outside a buffer; the outputs of their group mean nothing then, nor do those
+ * of sequences in no group. */
 typedef struct bl_kv_shared {
     const int32_t* group;  /* device [groups + 1], ascending from 0 to seqs */
     const int32_t* prefix; /* device [groups]                               */
@@ -606,14 +606,16 @@ typedef struct bl_kv_shared {
     int64_t max_prefix;
 } bl_kv_shared;
 
-/* Device workspace of bl_attention_shared (0: an argument is invalid, or there is nothing to do). */
+/* Device workspace of bl_attention_shared (0: none is needed, or an argument is invalid). */
 size_t bl_attention_shared_workspace_bytes(const bl_kv_cache* cache, const bl_kv_batch* batch,
                                            const bl_kv_shared* shared, int64_t q_heads);
 
 /* bl_attention without a window for such a batch: the keys and values of a
- * prefix are read for all queries of its group together.  The results are
- * those of bl_attention but for the order of the sums.  (A window leaves little
- * of a long prefix to see: bl_attention reads no more than that.)
+ * prefix are read for all queries of its group together, where the bounds
+ * make that worth its while (short prefixes, and prompts whose rows fill tiles
+ * of their own, are taken as bl_attention takes them).  The results are those
+ * of bl_attention but for the order of the sums.  (A window leaves little of a
+ * long prefix to see: bl_attention reads no more than that.)
  *   q, out, lse  as for bl_attention.
  * Errors: BL_ERR_NULL, BL_ERR_SHAPE (also groups * max_group below seqs, a
  * max_prefix past max_len), BL_ERR_ALIGN, BL_ERR_WORKSPACE, BL_ERR_HIP. */

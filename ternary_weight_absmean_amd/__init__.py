@@ -854,7 +854,7 @@ def bl_attention_shared_workspace_bytes(cache: KVCache, batch: KVBatch, shared: 
 def bl_attention_shared(cache: KVCache, batch: KVBatch, shared: KVShared, q: torch.Tensor, scale: float | None = None,
                         out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
                         workspace: torch.Tensor | None = None) -> torch.Tensor:
-    """bl_attention (without a window) of sequences that share prefixes, each of which is read once per group."""
+    """bl_attention (without a window) of sequences that share prefixes; one is read once per group where that pays."""
     q_heads = q.shape[1]
     shape = (batch.tokens, q_heads, cache.dim)
     qp, qt, qh = _heads(q, "q", shape)

@@ -469,8 +469,8 @@ bl::KvGroups groups_of(const bl_kv_shared* s) { return {s->group, s->prefix, s->
 size_t bl_attention_shared_workspace_bytes(const bl_kv_cache* cache, const bl_kv_batch* batch, const bl_kv_shared* shared,
                                            int64_t q_heads) {
   if (check_shared(cache, batch, shared, q_heads) != BL_OK || nothing_new(batch)) return 0;
-  return bl::attention_shared_workspace_bytes(view(cache), batch->tokens, batch->max_new, batch->max_len, q_heads,
-                                              groups_of(shared));
+  return bl::attention_shared_workspace_bytes(view(cache), batch->seqs, batch->tokens, batch->max_new, batch->max_len,
+                                              q_heads, groups_of(shared));
 }
 
 bl_status bl_attention_shared(const bl_kv_cache* cache, const bl_kv_batch* batch, const bl_kv_shared* shared,
@@ -480,14 +480,16 @@ bl_status bl_attention_shared(const bl_kv_cache* cache, const bl_kv_batch* batch
   if (bl_status st = check_shared(cache, batch, shared, q_heads)) return st;
   if (!(fabsf(scale) < INFINITY)) return BL_ERR_SHAPE;
   if (nothing_new(batch)) return BL_OK;  // empty tensors may carry NULL pointers
-  if (!q || !out || !shared->group || !shared->prefix || !workspace) return BL_ERR_NULL;
+  if (!q || !out || !shared->group || !shared->prefix) return BL_ERR_NULL;
   if (!aligned(q, 16) || !strides_ok(q_token_stride, q_head_stride) || !aligned(out, 16) || !aligned(lse, 4) ||
       !aligned(workspace, 16) || !aligned(shared->group, 4) || !aligned(shared->prefix, 4))
     return BL_ERR_ALIGN;
   const bl::KvView kv = view(cache);
   const bl::KvGroups groups = groups_of(shared);
-  if (bl::attention_shared_workspace_bytes(kv, batch->tokens, batch->max_new, batch->max_len, q_heads, groups) > workspace_bytes)
-    return BL_ERR_WORKSPACE;
+  const size_t need = bl::attention_shared_workspace_bytes(kv, batch->seqs, batch->tokens, batch->max_new, batch->max_len,
+                                                           q_heads, groups);
+  if (need > 0 && !workspace) return BL_ERR_NULL;
+  if (need > workspace_bytes) return BL_ERR_WORKSPACE;
   return from_hip(bl::launch_attention_shared(kv, step_of(batch), groups, batch->seqs, batch->tokens, batch->max_new,
                                               batch->max_len, q, q_token_stride, q_head_stride, (int)q_heads, scale, out, lse,
                                               workspace, (hipStream_t)stream));

@@ -1309,6 +1309,33 @@ SharedPlan make_shared_plan(const KvView& kv, int64_t tokens, int64_t max_new, i
   return p;
 }
 
+// Whether prefixes are taken together at all: what their tiles cost in each
+// sequence by itself against what they cost together, with the partial sums
+// (written and read at 5 TB/s) and 4 us for a launch that joins, 8 where one
+// sequence's keys would need no join.  A step of 64 keys of a tile of 16 rows takes
+// 1 ns of the chip per 64 elements, 1.5 where long keys are read again (they are
+// split then), of 128 rows 3.6, 5 or 13 ns for heads up to 64, 128, 256; tiles of
+// 128 rows fill less evenly together, by a tenth, by a fifth for heads of 65 to 128.
+// 64/8 heads of 128, together and apart: one group, 8 x 5 tokens after 2048 22 us
+// and 26, 24 x 20 after 12000 261 and 407, 8 x 100 after 128 76 and 23 (rows enough
+// for full tiles of their own); 8 groups, 8 tokens each after 512 19 and 14, after
+// 2048 28 and 45, 24 x 20 after 2048 518 and 445.
+bool worth_sharing(const SharedPlan& p, const KvView& kv, int64_t seqs, int64_t tokens, int64_t max_new, int64_t max_len,
+                   int64_t q_heads, int64_t groups, int64_t max_prefix) {
+  const double steps = (double)(max_prefix / kStep);
+  const int chunks = kv.dim <= 64 ? 1 : kv.dim <= 128 ? 2 : 4;
+  const double many = chunks == 1 ? 3.6 : chunks == 2 ? 5.0 : 13.0;
+  const Plan apart = make_plan(kv, seqs, max_new, max_len, q_heads, 0, 0);
+  const bool split = apart.splits > 1;
+  const double alone = (double)apart.tiles * steps * (apart.tile_rows == 16 ? (split ? 1.5 : 1.0) * chunks : many);
+  // Groups are seldom all as wide as the widest: tiles without rows cost nothing.
+  const double most = (double)kv.heads * ((double)tokens * (double)(q_heads / kv.heads) / (double)p.pre.tile_rows + (double)groups);
+  const bool few = p.pre.tile_rows == 16;
+  const double together = fmin((double)p.pre.tiles, most) * steps * (few ? 1.0 * chunks : many);
+  const double sums = (double)tokens * (double)q_heads * (double)p.slots() * kv.dim * 8 / 5000.0;
+  return alone > (together + sums) * (few ? 1.0 : chunks == 2 ? 1.2 : 1.1) + (split ? 4000.0 : 8000.0);
+}
+
 }  // namespace
 
 size_t attention_workspace_bytes(const KvView& kv, int64_t seqs, int64_t tokens, int64_t max_new, int64_t max_len,
@@ -1378,9 +1405,11 @@ hipError_t launch_attention(const KvView& kv, const KvStep& st, int64_t seqs, in
   return go(std::integral_constant<int, 4>{});
 }
 
-size_t attention_shared_workspace_bytes(const KvView& kv, int64_t tokens, int64_t max_new, int64_t max_len, int64_t q_heads,
-                                        const KvGroups& gr) {
+size_t attention_shared_workspace_bytes(const KvView& kv, int64_t seqs, int64_t tokens, int64_t max_new, int64_t max_len,
+                                        int64_t q_heads, const KvGroups& gr) {
   const SharedPlan p = make_shared_plan(kv, tokens, max_new, max_len, q_heads, gr.groups, gr.max_group, gr.max_prefix);
+  if (!worth_sharing(p, kv, seqs, tokens, max_new, max_len, q_heads, gr.groups, gr.max_prefix))
+    return attention_workspace_bytes(kv, seqs, tokens, max_new, max_len, q_heads);
   return (size_t)tokens * (size_t)q_heads * (size_t)p.slots() * (size_t)(kv.dim + 2) * 4;
 }
 
@@ -1388,6 +1417,8 @@ hipError_t launch_attention_shared(const KvView& kv, const KvStep& st, const KvG
                                    int64_t max_new, int64_t max_len, const uint16_t* q, int64_t qt, int64_t qh, int q_heads,
                                    float scale, uint16_t* out, float* lse, void* workspace, hipStream_t s) {
   const SharedPlan p = make_shared_plan(kv, tokens, max_new, max_len, q_heads, gr.groups, gr.max_group, gr.max_prefix);
+  if (!worth_sharing(p, kv, seqs, tokens, max_new, max_len, q_heads, gr.groups, gr.max_prefix))
+    return launch_attention(kv, st, seqs, tokens, max_new, max_len, q, qt, qh, q_heads, scale, 0, 0, out, lse, workspace, s);
   const Plan &pre = p.pre, &rest = p.rest;
   const bool any = gr.max_prefix >= kStep;
   const int64_t pre_blocks = any ? (pre.tiles * pre.splits + 7) / 8 * 8 : 0;

@@ -170,8 +170,8 @@ struct KvGroups {
   const int32_t *group, *prefix;
   int64_t groups, max_group, max_prefix;
 };
-size_t attention_shared_workspace_bytes(const KvView& kv, int64_t tokens, int64_t max_new, int64_t max_len, int64_t q_heads,
-                                        const KvGroups& gr);
+size_t attention_shared_workspace_bytes(const KvView& kv, int64_t seqs, int64_t tokens, int64_t max_new, int64_t max_len,
+                                        int64_t q_heads, const KvGroups& gr);
 hipError_t launch_attention_shared(const KvView& kv, const KvStep& st, const KvGroups& gr, int64_t seqs, int64_t tokens,
                                    int64_t max_new, int64_t max_len, const uint16_t* q, int64_t qt, int64_t qh, int q_heads,
                                    float scale, uint16_t* out, float* lse, void* workspace, hipStream_t s);

@@ -143,16 +143,23 @@ def test_attention_shared_refusals():
                 dict(heads=65536, q_heads=65536, tokens=1 << 18, max_new=1, max_len=64),
                 dict(scale=math.inf)):
         assert call(**bad) == BL_ERR_SHAPE, bad
-    for name in ("q", "out", "ws", "group", "prefix"):
+    for name in ("q", "out", "group", "prefix"):
         assert call(**{name: None}) == BL_ERR_NULL, name
         assert call(**{name: FAKE + 2}) == BL_ERR_ALIGN, name
+    assert call(ws=FAKE + 2) == BL_ERR_ALIGN
     for name in ("q", "out", "ws"):
         assert call(**{name: FAKE + 8}) == BL_ERR_ALIGN, name
     assert call(qt=100) == BL_ERR_ALIGN and call(lse=FAKE + 2) == BL_ERR_ALIGN
-    ((c, cp), (b, bp)), (s, sp) = args({})
+    long = dict(pages=4096, stride=2048, seqs=40, tokens=40, max_new=1, max_len=32768, max_group=20, max_prefix=32000)
+    ((c, cp), (b, bp)), (s, sp) = args(dict(long))
     need = lib.bl_attention_shared_workspace_bytes(cp, bp, sp, 4)
-    assert need > 0 and call(nbytes=need - 1) == BL_ERR_WORKSPACE
+    assert need > 0 and call(nbytes=need - 1, **long) == BL_ERR_WORKSPACE
+    assert call(ws=None, **long) == BL_ERR_NULL
+    assert need != lib.bl_attention_workspace_bytes(cp, bp, 4)  # the prefixes are taken together
     assert lib.bl_attention_shared_workspace_bytes(cp, bp, sp, 3) == 0
+    # a short prefix is not: what bl_attention needs
+    ((c, cp), (b, bp)), (s, sp) = args(dict(long, max_prefix=128))
+    assert lib.bl_attention_shared_workspace_bytes(cp, bp, sp, 4) == lib.bl_attention_workspace_bytes(cp, bp, 4)
 
 
 def test_logprobs_refusals():

@@ -43,6 +43,13 @@ class Answers(Case):
         return bl.KVShared(i32(group), i32(self.prefix), max(self.width), max(self.prefix) if most is None else most)
 
 
+def together(c, q_heads, shared=None):
+    """Whether the sizes are those for which prefixes are taken together."""
+    cache, batch = c.device()
+    return bl.bl_attention_shared_workspace_bytes(cache, batch, c.shared() if shared is None else shared, q_heads) != \
+        bl.bl_attention_workspace_bytes(cache, batch, q_heads)
+
+
 def check(c, q, scale=None, q_device=None, shared=None):
     cache, batch = c.device()
     dim = c.k.shape[3]
@@ -104,6 +111,101 @@ def test_long_prefixes(groups, n_heads, q_heads, dim, page):
     c = Answers(rng, groups, n_heads, dim, page)
     say(f"bl_attention_shared long groups={groups} dim={dim}")
     check(c, heads(rng, c.total, q_heads, dim))
+
+
+# heads, q heads, dim, page, (prefix, sequences, new tokens each) of one long group, a second beside it
+TOGETHER = [
+    (1, 4, 64, 16, (20000, 20, 1)), (2, 10, 128, 32, (6000, 16, 1)), (1, 3, 80, 64, (9000, 24, 2)), (3, 3, 16, 128, (9000, 40, 1)),
+    (1, 8, 48, 16, (12000, 30, 3)), (1, 20, 64, 64, (20000, 25, 4)), (2, 4, 256, 64, (4000, 16, 1)), (1, 2, 144, 32, (5000, 30, 5)),
+    (1, 1, 192, 256, (9000, 25, 1)), (2, 16, 128, 64, (4100, 33, 4)), (2, 8, 64, 64, (9000, 40, 6)), (1, 8, 256, 16, (3000, 60, 4)),
+    (2, 4, 128, 64, (9000, 6, 45))]
+
+
+@pytest.mark.parametrize("n_heads,q_heads,dim,page,first", TOGETHER)
+def test_prefixes_taken_together(n_heads, q_heads, dim, page, first):
+    """Sizes on the side of the rules where a group's rows share tiles, of 16 and of 128 rows; beside the long group
+    one that shares nothing, one with a shorter prefix, an empty sequence."""
+    rng = np.random.default_rng(dim + q_heads)
+    prefix, width, new = first
+    groups = [(prefix, [(37 * i) % 150 for i in range(width)], [1 + i % new for i in range(width)]), (0, [300], [1]),
+              (page * (600 // page) + 5, [0, 90, 3], [1, 0, new])]
+    c = Answers(rng, groups, n_heads, dim, page)
+    say(f"bl_attention_shared together {first} heads={n_heads}/{q_heads} dim={dim} page={page}")
+    assert together(c, q_heads)
+    q = heads(rng, c.total, q_heads, dim)
+    check(c, q)
+    c.table[:width, 3] = -1             # a hole in the prefix, and one sequence's own pages gone
+    c.table[min(2, width - 1), prefix // page:] = -1
+    c.va[c.table[0, 1]], c.ka[c.table[0, 2]] = 0, 0
+    check(c, q)
+
+
+def test_nan_in_a_prefix_taken_together():
+    rng = np.random.default_rng(6)
+    c = Answers(rng, [(9000, [i for i in range(30)], [1] * 30), (9000, [3, 70], [1, 1])], 2, 64, 64)
+    q = heads(rng, c.total, 8, 64)
+    assert together(c, 8)
+    say("bl_attention_shared NaN, together")
+
+    def attend():
+        cache, batch = c.device()
+        return bl.bl_attention_shared(cache, batch, c.shared(), bf16(_block.bits(q))).float().cpu().numpy()
+
+    clean = attend()
+    c.ka[c.table[0, 1], 1] = np.nan
+    out = attend()
+    assert np.isnan(out[:30, 4:]).all() and np.array_equal(out[30:], clean[30:]) and np.array_equal(out[:, :4], clean[:, :4])
+    c.ka[c.table[0, 1], 1] = 1.0
+    clean = attend()
+    c.va[c.table[31, -1 if c.table[31, -1] >= 0 else 141], 0] = np.inf  # the last sequence's own last page
+    q[3, 2, 5] = np.nan
+    out = attend()
+    assert np.isnan(out[31, :4]).all() and np.isnan(out[3, 2]).all()
+    out[31, :4], out[3, 2] = clean[31, :4], clean[3, 2]
+    assert np.array_equal(out, clean)
+
+
+def test_captured_and_odd_integers_together():
+    rng = np.random.default_rng(8)
+    c = Answers(rng, [(9000, [5 * i for i in range(20)], [1] * 20), (640, [3, 70], [1, 1])], 2, 64, 64)
+    q = bf16(_block.bits(heads(rng, c.total, 8, 64)))
+    cache, batch = c.device()
+    shared = c.shared()
+    assert together(c, 8)
+    say("bl_attention_shared captured, together")
+    ws = torch.empty(bl.bl_attention_shared_workspace_bytes(cache, batch, shared, 8), dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = bl.bl_attention_shared(cache, batch, shared, q, workspace=ws)
+        graphs.append((g, out))
+    prefix = shared.prefix.clone()
+    for i in range(4):
+        shared.prefix.copy_(prefix - 64 * i)  # the graph follows the device's integers
+        expect = bl.bl_attention_shared(cache, batch, shared, q)
+        ws.fill_(0xFF)
+        graphs[i % 2][0].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(graphs[i % 2][1], expect)
+    want = expect.float()
+    for i, (group, far) in enumerate((([0, 99, -5], [1 << 30, -3]), ([-7, 2, 5], [128, 640]), ([20, 1, 5], [0, 9000]), ([0, 0, 0], [64, 64]),
+                                      ([0, 20, 22], [9064, 1 << 30]))):
+        odd = bl.KVShared(i32(group), i32(far), 20, 9000)
+        need = bl.bl_attention_shared_workspace_bytes(cache, batch, odd, 8)
+        walled, out, lse = Walled((need,), torch.uint8), Walled(tuple(q.shape), torch.bfloat16), Walled(tuple(q.shape[:2]), torch.float32)
+        walled.t.zero_()
+        bl.bl_attention_shared(cache, batch, odd, q, out=out.t, lse=lse.t, workspace=walled.t)
+        torch.cuda.synchronize()
+        assert walled.intact() and out.intact() and lse.intact()
+    start = bl.KVBatch(batch.page_table, i32([-9, 1 << 30] + [5] * 20), batch.offsets, c.total, 1, batch.max_len)
+    need = bl.bl_attention_shared_workspace_bytes(cache, start, shared, 8)
+    walled, out = Walled((need,), torch.uint8), Walled(tuple(q.shape), torch.bfloat16)
+    walled.t.zero_()
+    bl.bl_attention_shared(cache, start, shared, q, out=out.t, workspace=walled.t)
+    torch.cuda.synchronize()
+    assert walled.intact() and out.intact() and torch.isfinite(want).all()
 
 
 @pytest.mark.parametrize("width", [1, 5, 40])
