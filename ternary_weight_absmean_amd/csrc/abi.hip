@@ -529,7 +529,9 @@ bl_status bl_kv_fork(const bl_kv_pool* pool, const int32_t* table, int64_t table
                      int64_t seqs, const int32_t* parent, int64_t children, int keep_parents, int32_t* table_out,
                      int32_t* length_out, int32_t* copies, int32_t* shortage, void* stream) {
   if (bl_status st = check_pool(pool, seqs, table_stride)) return st;
-  if (seqs > BL_MAX_FORK_SEQS || children < 0 || children > BL_MAX_FORK_SEQS || (table && table_out == table)) return BL_ERR_SHAPE;
+  if (seqs > BL_MAX_FORK_SEQS || children < 0 || children > BL_MAX_FORK_SEQS || (table && table_out == table) ||
+      (length && length_out == length))
+    return BL_ERR_SHAPE;
   if ((children == 0 && (keep_parents || seqs == 0)) || (seqs > 0 && table_stride == 0 && children == 0)) return BL_OK;
   if (!pool->refs || (seqs > 0 && (!length || (table_stride > 0 && !table))) ||
       (children > 0 && (!parent || !length_out || !copies || (table_stride > 0 && !table_out))))

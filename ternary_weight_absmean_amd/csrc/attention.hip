@@ -1295,7 +1295,7 @@ SharedPlan make_shared_plan(const KvView& kv, int64_t tokens, int64_t max_new, i
   pre.tile_rows = few < kFewWork && few * pre_steps * chunks < kFewWork ? 16 : kPromptRows;
   pre.row_tiles = (most * group + pre.tile_rows - 1) / pre.tile_rows;
   pre.tiles = groups * kv.heads * pre.row_tiles;
-  p.finish = rest.tile_rows == 16 && (pre.tile_rows != 16 || pre_steps == 0);
+  p.finish = rest.tile_rows == 16 && pre.tile_rows != 16;
   const int64_t all = p.finish ? pre.tiles : pre.tiles + rest.tiles;
   pre.teams = pre.tile_rows != 16 && kv.dim <= 128 && all < 256 ? 2 : 1;
   rest.teams = rest.tile_rows != 16 ? pre.teams : 1;
@@ -1420,8 +1420,7 @@ hipError_t launch_attention_shared(const KvView& kv, const KvStep& st, const KvG
   if (!worth_sharing(p, kv, seqs, tokens, max_new, max_len, q_heads, gr.groups, gr.max_prefix))
     return launch_attention(kv, st, seqs, tokens, max_new, max_len, q, qt, qh, q_heads, scale, 0, 0, out, lse, workspace, s);
   const Plan &pre = p.pre, &rest = p.rest;
-  const bool any = gr.max_prefix >= kStep;
-  const int64_t pre_blocks = any ? (pre.tiles * pre.splits + 7) / 8 * 8 : 0;
+  const int64_t pre_blocks = (pre.tiles * pre.splits + 7) / 8 * 8;
   const int64_t rest_blocks = (rest.tiles + 7) / 8 * 8 * rest.splits;
   if (!grid_fits(pre_blocks + rest_blocks, 2 * kThreads) || pre_blocks > 0x7FFFFFFF - 8 ||
       !grid_fits(rest.tiles * rest.tile_rows, kThreads))
@@ -1484,10 +1483,10 @@ hipError_t launch_attention_shared(const KvView& kv, const KvStep& st, const KvG
       return hipGetLastError();
     };
     hipError_t e;
-    if (pre_blocks > 0 && pre.tile_rows == rest.tile_rows) {
+    if (pre.tile_rows == rest.tile_rows) {
       e = launch(rest.tile_rows, rest.teams, pre_blocks, rest_blocks);
     } else {
-      e = pre_blocks > 0 ? launch(pre.tile_rows, pre.teams, pre_blocks, 0) : hipSuccess;
+      e = launch(pre.tile_rows, pre.teams, pre_blocks, 0);
       if (e == hipSuccess) e = launch(rest.tile_rows, rest.teams, 0, rest_blocks);
     }
     if (e != hipSuccess || (p.finish && rest.splits == 1)) return e;

@@ -50,14 +50,14 @@ def test_kv_grow_refusals():
 
 def test_kv_fork_refusals():
     def call(refs=FAKE, pages=100, page=16, table=FAKE, stride=4, length=FAKE, seqs=2, parent=FAKE, children=3, keep=0,
-             out=2 * FAKE, out_length=FAKE, copies=FAKE, shortage=None):
+             out=2 * FAKE, out_length=4 * FAKE, copies=FAKE, shortage=None):
         held, pp = pool(refs, pages, page)
         return lib.bl_kv_fork(pp, table, stride, length, seqs, parent, children, keep, out, out_length, copies, shortage, None)
 
     assert lib.bl_kv_fork(None, FAKE, 4, FAKE, 2, FAKE, 3, 0, FAKE, FAKE, FAKE, None, None) == BL_ERR_NULL
     check_pool(call)
     for bad in (dict(seqs=-1), dict(seqs=8193), dict(children=-1), dict(children=8193), dict(stride=-1), dict(stride=1 << 26),
-                dict(out=FAKE)):
+                dict(out=FAKE), dict(out_length=FAKE)):
         assert call(**bad) == BL_ERR_SHAPE, bad
     for name in ("table", "length", "parent", "out", "out_length", "copies"):
         assert call(**{name: None}) == BL_ERR_NULL, name

@@ -118,7 +118,10 @@ TOGETHER = [
     (1, 4, 64, 16, (20000, 20, 1)), (2, 10, 128, 32, (6000, 16, 1)), (1, 3, 80, 64, (9000, 24, 2)), (3, 3, 16, 128, (9000, 40, 1)),
     (1, 8, 48, 16, (12000, 30, 3)), (1, 20, 64, 64, (20000, 25, 4)), (2, 4, 256, 64, (4000, 16, 1)), (1, 2, 144, 32, (5000, 30, 5)),
     (1, 1, 192, 256, (9000, 25, 1)), (2, 16, 128, 64, (4100, 33, 4)), (2, 8, 64, 64, (9000, 40, 6)), (1, 8, 256, 16, (3000, 60, 4)),
-    (2, 4, 128, 64, (9000, 6, 45))]
+    (2, 4, 128, 64, (9000, 6, 45)), (4, 20, 208, 64, (3000, 6, 70)), (4, 64, 64, 32, (1500, 12, 70)), (4, 64, 112, 64, (1500, 6, 70)),
+    (1, 16, 208, 64, (3000, 12, 70)), (1, 16, 208, 16, (6000, 3, 70)), (2, 32, 208, 64, (3000, 3, 70)), (4, 20, 112, 64, (6000, 3, 40)),
+    (4, 20, 208, 64, (700, 6, 70)), (4, 64, 64, 16, (700, 12, 70)), (4, 64, 112, 64, (700, 6, 70)), (1, 8, 64, 64, (16000, 24, 9)),
+    (1, 8, 128, 64, (12000, 30, 9)), (1, 9, 80, 16, (12000, 30, 8))]
 
 
 @pytest.mark.parametrize("n_heads,q_heads,dim,page,first", TOGETHER)
@@ -138,6 +141,16 @@ def test_prefixes_taken_together(n_heads, q_heads, dim, page, first):
     c.table[min(2, width - 1), prefix // page:] = -1
     c.va[c.table[0, 1]], c.ka[c.table[0, 2]] = 0, 0
     check(c, q)
+
+
+@pytest.mark.parametrize("dim,page", [(64, 64), (128, 32)])
+def test_long_rests_behind_a_prefix(dim, page):
+    """Prefix and rests both with many rows and steps, on workgroups of two teams."""
+    rng = np.random.default_rng(dim)
+    c = Answers(rng, [(20000, [2100 + 7 * i for i in range(30)], [9 - i % 2 for i in range(30)])], 1, dim, page)
+    say(f"bl_attention_shared long rests dim={dim}")
+    assert together(c, 8)
+    check(c, heads(rng, c.total, 8, dim))
 
 
 def test_nan_in_a_prefix_taken_together():
