@@ -825,7 +825,7 @@ __global__ __launch_bounds__(kThreads * kTeams, DC <= 2 ? 2 : 1) void k_attn_pro
   // products and their softmax in turn 883 cycles, mixed 693).  Wave priorities:
   // staging, which other waves wait for, before the values' products before the
   // rest (6000 tokens, 20/5 heads: 223 us against 245 without; 6 x 509 under a
-  // a.window of 1024 52.7 against 55.8).
+  // window of 1024 52.7 against 55.8).
   v16i high, lo;   // the next half's scores
   v8h pf[2];       // the half before: its probabilities,
   uint4 vf[2][kTiles];  // and its values
