@@ -504,8 +504,8 @@ bl_status bl_attention(const bl_kv_cache* cache, const bl_kv_batch* batch, const
  * Pages are handed out lowest number first, to requests in the order of
  * sequences and, within one, of positions: equal inputs give equal results.
  * shortage: NULL, or a device integer to which the number of requests that
- * found no free page is added (their entries stay, or become, -1); the host
- * clears it.  Counts that do not agree with the tables give no access outside
+ * found no free page is added (their entries stay, or become, -1, but for
+ * those of shared pages in bl_kv_grow); the host clears it.  Counts that do not agree with the tables give no access outside
  * a buffer; no count goes below 0. */
 #define BL_MAX_POOL_PAGES (1 << 24)
 #define BL_MAX_FORK_SEQS 8192
@@ -522,11 +522,14 @@ typedef struct bl_kv_pool {
  *   copies  NULL, or out device [seqs][3] for bl_kv_copy: a part-filled page in
  *           which a sequence goes on writing (position start[s]) and that others
  *           hold too is copied onto a fresh one, {source, target, tokens},
- *           {-1, -1, 0} elsewhere; of sequences of the batch that share it, the
- *           last one keeps it if nobody else does.  Such pages come from
+ *           {-1, -1, 0} elsewhere; of sequences of the batch that write in it, the
+ *           last one keeps it if nobody else holds it then.  Such pages come from
  *           cutting back (bl_kv_free with keep) into pages that a fork shares.
- *           Where no page was free for a copy the entry stays as it is, shared:
- *           such a sequence must not be written.
+ *           Where no page was free for a copy the entry stays as it is, shared,
+ *           and copies has {source, -1, 0}, which bl_kv_copy passes over: such a
+ *           sequence must not be written.  That is so for the last one too if one
+ *           before it got no copy.  Each of them is counted in shortage; once pages
+ *           are free again, the same call goes on from there.
  * Errors: BL_ERR_NULL, BL_ERR_SHAPE (also when sequences times the pages that
  * max_new tokens may enter pass 2^24, or seqs passes BL_MAX_FORK_SEQS with
  * copies), BL_ERR_ALIGN, BL_ERR_HIP. */

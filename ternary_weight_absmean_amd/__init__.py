@@ -758,8 +758,8 @@ def bl_kv_grow(pool: KVPool, batch: KVBatch, copies: torch.Tensor | None = None,
                shortage: torch.Tensor | None = None) -> None:
     """Gives pages to the entries of the batch's page table in which its new tokens stand and that have none.
     ``copies`` (int32 [seqs][3], optional) takes what bl_kv_copy has to copy where a sequence would go on writing in a
-    page that others hold too; ``shortage`` (int32 [1], optional) grows by the number of requests for which no page
-    was free."""
+    page that others hold too: (source, target, tokens), (source, -1, 0) if it must not be written since no page was
+    free; ``shortage`` (int32 [1], optional) grows by the number of requests for which none was."""
     _check("bl_kv_grow", _lib.bl_kv_grow(
         pool.address, batch.address, _dense(copies, "copies", torch.int32, (batch.page_table.shape[0], 3)),
         _dense(shortage, "shortage", torch.int32, (1,)), _stream(pool.refs.device)))

@@ -37,12 +37,13 @@ class Pool:
             for i in range(a // self.page, (a + n - 1) // self.page + 1):
                 shared = copies is not None and i * self.page < a and i < len(row) and self.there(row[i])
                 if shared and self.refs[row[i]] - left.count(row[i]) > 1:
-                    left.append(row[i])
-                    if free:
+                    if free:  # a sequence that gets no page goes on holding the shared one
+                        left.append(row[i])
                         copies[-1] = (row[i], free.pop(), a % self.page)
                         row[i] = copies[-1][1]
                         self.refs[row[i]] = 1
                     else:
+                        copies[-1] = (row[i], -1, 0)
                         short += 1
                 elif i < len(row) and not self.there(row[i]):
                     if free:
@@ -50,8 +51,8 @@ class Pool:
                         self.refs[row[i]] = 1
                     else:
                         short += 1
-        for c in copies or []:
-            self.release(c[0])
+        for e in left:
+            self.release(e)
         return short
 
     def fork(self, table, length, parent, keep):
