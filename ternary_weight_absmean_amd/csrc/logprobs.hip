@@ -7,8 +7,9 @@
 // B's rounding is the same in every d, and known: delta = fma(M, c, -B).  With
 // log_s = (log2 S - delta) ln 2,
 //   lse = scale M + log_s,  logprob_j = scale (x_j - M) - log_s.
-// Where M c is not well inside fp32's range (rows of the type's lowest value),
-// d_j = (x_j - M) c instead.  All sums are fp32.
+// From |M c| = 2^28 on, where delta is no small exponent any more (up to rows of
+// the type's lowest value, where M c may overflow), d_j = (x_j - M) c instead, in a
+// second reading.  All sums are fp32.
 //
 // A row is cut into chunks that one workgroup each holds in registers: one
 // reading of the logits gives the chunk's maximum, then (from the registers) S, W and
@@ -112,11 +113,16 @@ __device__ __forceinline__ int wave_rth(int v, int top, int r) {
   return top;
 }
 
-// What is taken off the exponents of a row or chunk whose maximum is top.
+// What is taken off the exponents of a row or chunk whose maximum is top: b, or
+// where that is far, top * c itself.
 struct Shift {
   float b;
-  bool far;  // top * c near the end of fp32's range, or infinite
-  __device__ Shift(float top, float c) : b(top == -INFINITY ? 0.0f : top * c), far(!(fabsf(b) < 0x1p126f)) {}
+  bool far;
+  __device__ Shift(float top, float c) : b(top == -INFINITY ? 0.0f : top * c), far(!(fabsf(b) < 0x1p28f)) {}
+  // top * c - b, exactly; 0 where top * c may be infinite
+  __device__ float rest(float top, float c) const {
+    return fabsf(b) < 0x1p126f && top != -INFINITY ? __builtin_fmaf(top, c, -b) : 0.0f;
+  }
 };
 
 struct Final {
@@ -124,7 +130,7 @@ struct Final {
   // max, S and W of a whole row; S is 0 where nothing is possible
   __device__ Final(const LogArgs& a, float most, float s, float w) : top(most), scale(a.scale) {
     const Shift shift(most, a.c);
-    const float log2_s = __log2f(s), delta = shift.far || most == -INFINITY ? 0.0f : __builtin_fmaf(most, a.c, -shift.b);
+    const float log2_s = __log2f(s), delta = shift.far ? 0.0f : shift.rest(most, a.c);
     log_s = (log2_s - delta) * kLn2;
     entropy = s == 0.0f ? 0.0f : (log2_s - w / s) * kLn2;
     lse = s == 0.0f ? -INFINITY : __builtin_fmaf(top, scale, log_s);
@@ -357,9 +363,15 @@ __global__ __launch_bounds__(kJoinThreads) void k_logprobs_join(LogArgs a) {
   float4 part = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
   if (lane < a.chunks) part = *reinterpret_cast<const float4*>(a.stats + 4 * (row * a.chunks + lane));
   const float top = value_of(wave_reduce<true>(order_of(part.x)));  // every wave has the row's
-  // S and W relative to the row's maximum
-  const Shift whole(top, a.c);
-  const float shift = part.x == -INFINITY ? 0.0f : whole.far ? (part.x - top) * a.c : part.x * a.c - whole.b;
+  // S and W relative to the row's maximum: from what was taken off in the chunk to
+  // what is in the row, which may be far where the other is not
+  const Shift whole(top, a.c), own(part.x, a.c);
+  float shift = own.b - whole.b;
+  if (own.far && whole.far)
+    shift = (part.x - top) * a.c;
+  else if (own.far || whole.far)
+    shift += own.far ? own.rest(part.x, a.c) : -whole.rest(top, a.c);
+  if (part.x == -INFINITY) shift = 0.0f;
   const float e = __builtin_amdgcn_exp2f(shift);
   const float s = wave_sum(part.y * e), w = wave_sum(e * __builtin_fmaf(part.y, fmaxf(shift, -300.0f), part.z));
   const Final f(a, top, s, w);
