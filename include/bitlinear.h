@@ -661,7 +661,9 @@ bl_status bl_logprobs(const void* x, int type, int64_t m, int64_t n, int64_t row
 
 /* Gradient of sum_i (dlogprob_i logprob_i + dentropy_i entropy_i + dlse_i lse_i):
  *   dx_j = scale * (dlogprob ([j = t] - p_j) + dlse p_j - dentropy p_j (log p_j + entropy)),
- * from the logits and the lse and entropy that bl_logprobs gave for them.
+ * from the logits and the lse and entropy that bl_logprobs gave for them.  Where
+ * |lse| is 64 or more (fp32; 512 for bf16) its rounding would show in every p: the
+ * row's sum is taken again then, by one workgroup per row.
  *   dlogprob (with target), dentropy (with entropy), dlse  fp32 [m], each NULL
  *            for zeros, not all.  A row whose gradients are all zero (or where
  *            no token can occur) gets zeros whatever its logits are.

@@ -416,7 +416,17 @@ __global__ __launch_bounds__(kJoinThreads) void k_logprobs_join(LogArgs a) {
 // zero, and rows where nothing is possible, get zeros without being read.  The
 // last rows come first: the forward call has left them in the Infinity Cache;
 // stores (and loads, which are the last of a row) go past the caches.  4096 x 128256
-// bf16, forward and this: 558 us, 605 in ascending order through the caches.
+// bf16, forward and this: 550 us, 605 in ascending order through the caches.
+//
+// lse is one fp32 number, so every p of a row is off by up to half its unit: 2^-19
+// at 64, a factor n for a row of the type's lowest value, where log n is lost.
+// From kFarLse on a row's sum of exponentials is taken again, by one of its
+// workgroups, which then does the whole row (it may be overwritten in place): p_j =
+// 2^(d_j - log2 S) with d_j from any one shift near the maximum.  Row r's is that of
+// chunk r % chunks: the first ones may all lie on one XCD (4096 x 128256 bf16 at
+// logits around 1000: 653 us, 4032 with them, 394 of a batch around 0).
+// Below, the unit is within the exponent's own roundings (fp32) or under a
+// sixtieth of the output's (bf16).
 struct GradArgs {
   const char* x;
   int64_t x_stride;
@@ -428,11 +438,17 @@ struct GradArgs {
   const float *lse, *entropy, *g, *gh, *gz;
 };
 
+template <bool kBf16>
+constexpr float kFarLse = kBf16 ? 512.0f : 64.0f;
+// From here on half a unit of lse is no small exponent: the maximum is looked for.
+constexpr float kLostLse = 0x1p24f;
+
 constexpr int kGradThreads = 256;
 template <bool kBf16, int E, bool kAligned>
 __global__ __launch_bounds__(kGradThreads) void k_logprobs_backward(GradArgs a) {
   typedef Pieces<kBf16> P;
-  constexpr int kPer = P::kPer;
+  constexpr int kPer = P::kPer, kWaves = kGradThreads / 64;
+  __shared__ float part[kWaves];
   const uint32_t block = gridDim.x - 1 - blockIdx.x;
   const int64_t row = block / a.chunks;
   const int chunk = (int)(block - row * a.chunks), tid = threadIdx.x;
@@ -446,32 +462,18 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_backward(GradArgs a) 
   const float plain = a.scale * (gz - g - (gh != 0.0f ? gh * a.entropy[row] : 0.0f)), slope = -a.scale * gh * kLn2;
   const float hit = zero ? 0.0f : a.scale * g;
   char* out = a.dx + row * a.dx_stride;
-  auto value = [&](float x) {
-    const float d = __builtin_fmaf(x, a.scale, -lse) * kLog2e;
-    return __builtin_amdgcn_exp2f(d) * __builtin_fmaf(slope, fmaxf(d, -300.0f), plain);
-  };
+  auto weigh = [&](float d) { return __builtin_amdgcn_exp2f(d) * __builtin_fmaf(slope, fmaxf(d, -300.0f), plain); };
   auto store = [&](int j, float v) {
     if (kBf16)
       reinterpret_cast<uint16_t*>(out)[j] = f32_to_bf16_rne(v);
     else
       reinterpret_cast<float*>(out)[j] = v;
   };
-  if (chunk == 0 && tid < p.edges()) {
-    const int j = p.edge(tid);
-    store(j, (zero ? 0.0f : value(p.at(j))) + (j == t ? hit : 0.0f));
-  }
-  v4u data[E];
-  if (!zero && v0 < v1) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) data[i] = __builtin_nontemporal_load(p.vec(min(v0 + i * kGradThreads + tid, v1 - 1)));
-  }
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int v = v0 + i * kGradThreads + tid, first = p.head + v * kPer;
-    if (v >= v1) continue;
+  auto store_piece = [&](int v, const v4u& data, auto value) {
+    const int first = p.head + v * kPer;
     float y[kPer];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) y[j] = zero ? 0.0f : value(element<kBf16>(data[i], j));
+    for (int j = 0; j < kPer; ++j) y[j] = value(element<kBf16>(data, j));
     if ((uint32_t)(t - first) < (uint32_t)kPer) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) y[j] += first + j == t ? hit : 0.0f;
@@ -485,6 +487,76 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_backward(GradArgs a) 
 #pragma unroll
       for (int j = 0; j < kPer; ++j) store(first + j, y[j]);
     }
+  };
+  const bool alone = !zero && fabsf(lse) >= kFarLse<kBf16>;
+  const int leader = alone ? (int)(row % a.chunks) : 0;
+  const bool has_edge = chunk == leader && tid < p.edges();
+  const int edge = has_edge ? p.edge(tid) : 0;
+
+  if (alone) {
+    if (chunk != leader) return;
+    const float at_edge = has_edge ? p.at(edge) : -INFINITY;
+    auto pieces = [&](auto f) {  // E at a time
+#pragma clang loop unroll(disable)
+      for (int base = tid; base < p.vecs; base += E * kGradThreads) {
+        v4u d[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) d[i] = *p.vec(min(base + i * kGradThreads, p.vecs - 1));
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if (base + i * kGradThreads < p.vecs) f(base + i * kGradThreads, d[i]);
+      }
+    };
+    const float c = a.scale * kLog2e;
+    float top = at_edge, b = lse * kLog2e;
+    bool far = false;
+    if (fabsf(lse) >= kLostLse) {
+      pieces([&](int, const v4u& d) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) top = fmaxf(top, element<kBf16>(d, j));
+      });
+      top = value_of(wave_reduce<true>(order_of(top)));
+      if ((tid & 63) == 0) part[tid >> 6] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, part[w]);
+      __syncthreads();  // part is written again
+      const Shift shift(top, c);
+      b = shift.b;
+      far = shift.far;
+    }
+    auto exponent = [&](float x) { return far ? (x - top) * c : __builtin_fmaf(x, c, -b); };
+    double all = __builtin_amdgcn_exp2f(exponent(at_edge));  // a thread's sum is a long one
+    pieces([&](int, const v4u& d) {
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) s += __builtin_amdgcn_exp2f(exponent(element<kBf16>(d, j)));
+      all += s;
+    });
+    const float s = wave_sum((float)all);
+    if ((tid & 63) == 0) part[tid >> 6] = s;
+    __syncthreads();
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) sum += part[w];
+    const float log2_s = __log2f(sum);
+    auto value = [&](float x) { return weigh(exponent(x) - log2_s); };
+    if (has_edge) store(edge, value(at_edge) + (edge == t ? hit : 0.0f));
+    pieces([&](int v, const v4u& d) { store_piece(v, d, value); });
+    return;
+  }
+
+  auto value = [&](float x) { return zero ? 0.0f : weigh(__builtin_fmaf(x, a.scale, -lse) * kLog2e); };
+  if (has_edge) store(edge, (zero ? 0.0f : value(p.at(edge))) + (edge == t ? hit : 0.0f));
+  v4u data[E];
+  if (!zero && v0 < v1) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) data[i] = __builtin_nontemporal_load(p.vec(min(v0 + i * kGradThreads + tid, v1 - 1)));
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int v = v0 + i * kGradThreads + tid;
+    if (v < v1) store_piece(v, data[i], value);
   }
 }
 
