@@ -136,7 +136,10 @@ struct Final {
     lse = s == 0.0f ? -INFINITY : __builtin_fmaf(top, scale, log_s);
   }
   __device__ float logprob(float x) const {
-    return x == -INFINITY && log_s == log_s ? -INFINITY : __builtin_fmaf(x - top, scale, -log_s);
+    if (x == -INFINITY && log_s == log_s) return -INFINITY;
+    const float d = x - top;
+    if (d == -INFINITY) return __builtin_fmaf(x, scale, -(top * scale)) - log_s;  // scale d may be finite all the same
+    return __builtin_fmaf(d, scale, -log_s);
   }
 };
 

@@ -42,7 +42,8 @@ def gradient(x, target, g, gh, gz, scale, bf16):
     bound = scale * r["p"] * (size * (off + 8 * U32) + np.abs(gh) * (r["entropy_bound"][:, None] + off))
     hit = np.zeros((m, n))
     hit[np.arange(m)[known], np.asarray(target)[known]] = 1.0
-    bound = bound + 4 * U32 * scale * np.abs(g) * hit
+    # p is held in fp32: one below 2^-126 may be 0, which takes at most 2^-126 off p, times what p is multiplied by
+    bound = bound + 4 * U32 * scale * np.abs(g) * hit + 2.0 ** -126 * scale * size
     return want, bound + (U16 if bf16 else U32) * (np.abs(want) + bound) + 2.0 ** -120
 
 
