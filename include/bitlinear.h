@@ -648,7 +648,7 @@ enum { BL_BF16 = 0, BL_FP32 = 1 };
 size_t bl_logprobs_workspace_bytes(int64_t m, int64_t n, int type, int64_t top);
 
 /*   x        [m][n] bf16 or fp32 (type), rows row_stride elements apart (>= n); aligned to its elements only.
- *   scale    > 0, finite: 1 / temperature.
+ *   scale    > 0, at most 2^127: 1 / temperature.
  *   target   [m] int32, needed for logprob only.
  *   logprob, lse, entropy  out fp32 [m], each NULL to skip it.
  *   top      0 .. BL_MAX_TOP; top_id out int32 [m][top], top_logprob out fp32 [m][top].

@@ -595,7 +595,7 @@ namespace {
 
 bl_status check_logits(int type, int64_t m, int64_t n, int64_t stride, float scale) {
   if ((type != BL_BF16 && type != BL_FP32) || m < 0 || m > BL_MAX_M || n < 1 || n > BL_MAX_VOCABULARY || stride < n ||
-      !product_ok(m, stride) || !(scale > 0.0f && scale < INFINITY))
+      !product_ok(m, stride) || !(scale > 0.0f && scale <= 0x1p127f))  // times log2 e, still finite
     return BL_ERR_SHAPE;
   return BL_OK;
 }
