@@ -548,12 +548,13 @@ bl_status bl_kv_grow(const bl_kv_pool* pool, const bl_kv_batch* batch, int32_t* 
  *                 itself).  `table` is not changed, its rows mean nothing then.
  *   table         device [seqs][table_stride]; length device [seqs].
  *   parent        device [children].
- *   table_out     out device [children][table_stride], not `table`.
- *   length_out    out device [children]: the parents' lengths; not `length`.
+ *   table_out     out device [children][table_stride].
+ *   length_out    out device [children]: the parents' lengths.
  *   copies        out device [children][3].
- * seqs and children are at most BL_MAX_FORK_SEQS.
- * Errors: BL_ERR_NULL, BL_ERR_SHAPE (also table_out = table, length_out =
- * length), BL_ERR_ALIGN, BL_ERR_HIP. */
+ * seqs and children are at most BL_MAX_FORK_SEQS.  The outputs share no element
+ * with each other or with what else the call reads or writes.
+ * Errors: BL_ERR_NULL, BL_ERR_SHAPE (also outputs that share elements),
+ * BL_ERR_ALIGN, BL_ERR_HIP. */
 bl_status bl_kv_fork(const bl_kv_pool* pool, const int32_t* table, int64_t table_stride, const int32_t* length,
                      int64_t seqs, const int32_t* parent, int64_t children, int keep_parents, int32_t* table_out,
                      int32_t* length_out, int32_t* copies, int32_t* shortage, void* stream);

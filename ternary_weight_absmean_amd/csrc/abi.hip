@@ -497,6 +497,12 @@ bl_status bl_attention_shared(const bl_kv_cache* cache, const bl_kv_batch* batch
 
 namespace {
 
+// Whether n elements from a on and m from b on have one in common.
+bool share_elements(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return n > 0 && m > 0 && x < y + 4 * (uintptr_t)m && y < x + 4 * (uintptr_t)n;
+}
+
 // A pool, and a table of `seqs` rows that goes with it.
 bl_status check_pool(const bl_kv_pool* pool, int64_t seqs, int64_t stride) {
   if (!pool) return BL_ERR_NULL;
@@ -539,6 +545,13 @@ bl_status bl_kv_fork(const bl_kv_pool* pool, const int32_t* table, int64_t table
   if (!aligned(pool->refs, 16) || !aligned(table, 4) || !aligned(length, 4) || !aligned(parent, 4) ||
       !aligned(table_out, 4) || !aligned(length_out, 4) || !aligned(copies, 4) || !aligned(shortage, 4))
     return BL_ERR_ALIGN;
+  // workgroups that run at once write the outputs and read the rest
+  const struct { const int32_t* at; int64_t n; } parts[] = {
+      {table_out, children * table_stride}, {length_out, children}, {copies, 3 * children}, {table, seqs * table_stride},
+      {length, seqs}, {parent, children}, {pool->refs, pool->pages}, {shortage, shortage ? 1 : 0}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 8; ++j)
+      if (share_elements(parts[i].at, parts[i].n, parts[j].at, parts[j].n)) return BL_ERR_SHAPE;
   return from_hip(bl::launch_kv_fork(pool->refs, pool->pages, pool->page_tokens, table, table_stride, length, seqs, parent,
                                      children, keep_parents != 0, table_out, length_out, copies, shortage,
                                      (hipStream_t)stream));
