@@ -669,8 +669,10 @@ bl_status bl_logprobs(const void* x, int type, int64_t m, int64_t n, int64_t row
  *            for zeros, not all.  A row whose gradients are all zero (or where
  *            no token can occur) gets zeros whatever its logits are.
  *   dx       out [m][n] of x's type, rows dx_stride elements apart; may be x
- *            (with dx_stride = row_stride).  Between rows nothing is written.
- * Errors: BL_ERR_NULL, BL_ERR_SHAPE, BL_ERR_ALIGN, BL_ERR_HIP. */
+ *            (with dx_stride = row_stride), and has no element of x otherwise.
+ *            Between rows nothing is written.
+ * Errors: BL_ERR_NULL, BL_ERR_SHAPE (also rows of dx that begin inside those of
+ * x, of the same stride), BL_ERR_ALIGN, BL_ERR_HIP. */
 bl_status bl_logprobs_backward(const void* x, int type, int64_t m, int64_t n, int64_t row_stride, float scale,
                                const int32_t* target, const float* lse, const float* entropy, const float* dlogprob,
                                const float* dentropy, const float* dlse, void* dx, int64_t dx_stride, void* stream);

@@ -613,6 +613,15 @@ bl_status check_logits(int type, int64_t m, int64_t n, int64_t stride, float sca
   return BL_OK;
 }
 
+// Whether rows of n elements, `stride` apart, at two places have elements in
+// common without being the same rows.
+bool rows_cross(const void* a, const void* b, int64_t m, int64_t n, int64_t stride, int64_t size) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  const uint64_t apart = x < y ? y - x : x - y, row = (uint64_t)(m > 1 ? stride : n) * size, length = (uint64_t)n * size;
+  const uint64_t rows = apart / row, rest = apart % row;
+  return apart > 0 && ((rows < (uint64_t)m && rest < length) || (rows + 1 < (uint64_t)m && row - rest < length));
+}
+
 }  // namespace
 
 size_t bl_logprobs_workspace_bytes(int64_t m, int64_t n, int type, int64_t top) {
@@ -650,6 +659,7 @@ bl_status bl_logprobs_backward(const void* x, int type, int64_t m, int64_t n, in
   if (!aligned(x, size) || !aligned(dx, size) || !aligned(target, 4) || !aligned(lse, 4) || !aligned(entropy, 4) ||
       !aligned(dlogprob, 4) || !aligned(dentropy, 4) || !aligned(dlse, 4))
     return BL_ERR_ALIGN;
+  if ((m == 1 || dx_stride == row_stride) && rows_cross(x, dx, m, n, row_stride, (int64_t)size)) return BL_ERR_SHAPE;
   return from_hip(bl::launch_logprobs_backward(x, type == BL_BF16, m, n, row_stride, scale, target, lse, entropy, dlogprob,
                                                dentropy, dlse, dx, dx_stride, (hipStream_t)stream));
 }
