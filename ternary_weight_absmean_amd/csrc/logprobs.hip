@@ -7,9 +7,11 @@
 // B's rounding is the same in every d, and known: delta = fma(M, c, -B).  With
 // log_s = (log2 S - delta) ln 2,
 //   lse = scale M + log_s,  logprob_j = scale (x_j - M) - log_s.
-// From |M c| = 2^28 on, where delta is no small exponent any more (up to rows of
-// the type's lowest value, where M c may overflow), d_j = (x_j - M) c instead, in a
-// second reading.  All sums are fp32.
+// From |M c| = 2^30 on (up to rows of the type's lowest value, where M c may
+// overflow), fp32 numbers next to M are at least 2^6 away in d, so that only
+// elements equal to M count: c is a power of two near scale log2 e then, for which
+// M c and d are exact.  Below, delta is at most 32, which W / S is rounded at; it
+// would leave the exponents' range from 2^31 on.  All sums are fp32.
 //
 // A row is cut into chunks that one workgroup each holds in registers: one
 // reading of the logits gives the chunk's maximum, then (from the registers) S, W and
@@ -120,11 +122,24 @@ __device__ __forceinline__ int wave_rth(int v, int top, int r) {
 struct Shift {
   float b;
   bool far;
-  __device__ Shift(float top, float c) : b(top == -INFINITY ? 0.0f : top * c), far(!(fabsf(b) < 0x1p28f)) {}
+  __device__ Shift(float top, float c) : b(top == -INFINITY ? 0.0f : top * c), far(!(fabsf(b) < 0x1p30f)) {}
   // top * c - b, exactly; 0 where top * c may be infinite
   __device__ float rest(float top, float c) const {
     return fabsf(b) < 0x1p126f && top != -INFINITY ? __builtin_fmaf(top, c, -b) : 0.0f;
   }
+};
+
+// The exponents d = x * c - b of such a row or chunk, for its sums.
+struct Exponents {
+  float c, b;
+  __device__ Exponents(const Shift& shift, float top, float c_) : c(c_), b(shift.b) {
+    if (!shift.far) return;
+    // more than c, so that nothing next to top counts, or less, so that nothing overflows
+    const float power = __int_as_float(__float_as_int(c_) & 0x7F800000);
+    c = fabsf(b) < 0x1p100f ? fminf(power, 0x1p125f) * 4.0f : power * 0.5f;
+    b = top * c;
+  }
+  __device__ float operator()(float x) const { return __builtin_fmaf(x, c, -b); }
 };
 
 struct Final {
@@ -221,14 +236,13 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogArgs a) {
     limit = fmaxf(value_of(max(least, order_of(-INFINITY))), kLowest);  // -infinity is no candidate
   }
 
-  const Shift shift(top, a.c);
+  const Exponents exponent(Shift(top, a.c), top, a.c);
   float s = 0.0f, w = 0.0f;
-  auto add_power = [&](float d) {
-    const float e = __builtin_amdgcn_exp2f(d);
+  auto add = [&](float x) {
+    const float d = exponent(x), e = __builtin_amdgcn_exp2f(d);
     s += e;
     w = __builtin_fmaf(e, fmaxf(d, -300.0f), w);  // 0 * -infinity is 0 here
   };
-  auto add = [&](float x) { add_power(__builtin_fmaf(x, a.c, -shift.b)); };
   // This thread's elements, each with its index, read again: the rare passes
   // over them take no registers from the first.
   auto each = [&](auto f) {
@@ -277,10 +291,6 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogArgs a) {
     }
   }
   asm("" : "+v"(s), "+v"(w));  // summed here, not behind the branch with all terms kept until there
-  if (shift.far) {
-    s = w = 0.0f;
-    each([&](float x, uint32_t) { add_power((x - top) * a.c); });
-  }
   s = wave_sum(s);
   w = wave_sum(w);
   if (lane == 0) {
@@ -530,6 +540,7 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_backward(GradArgs a) 
       b = shift.b;
       far = shift.far;
     }
+    // every weight's own here, however small
     auto exponent = [&](float x) { return far ? (x - top) * c : __builtin_fmaf(x, c, -b); };
     double all = __builtin_amdgcn_exp2f(exponent(at_edge));  // a thread's sum is a long one
     pieces([&](int, const v4u& d) {
