@@ -189,7 +189,7 @@ def test_rests_that_join_the_prefix_themselves_beside_longer_ones(n_heads, q_hea
     check(c, heads(rng, c.total, q_heads, dim))
 
 
-# (pages, heads, page, dim) of more than 2^32 bytes of keys; (sequences, rows of a group) for the kernels of 16 and of 128 rows
+# one token each: the prefix in tiles of 16 rows; 12 tokens of 40 sequences: of 128
 @pytest.mark.parametrize("seqs,new", [(12, 1), (40, 12)])
 def test_cache_past_two_to_the_32_bytes(seqs, new):
     pages, n_heads, page, dim, q_heads, shared_pages = 70000, 4, 64, 256, 8, 80

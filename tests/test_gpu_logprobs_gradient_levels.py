@@ -104,8 +104,8 @@ def test_gradients_of_rows_of_the_lowest_value(n, is_bf16):
 
 
 def test_gradients_at_a_level_against_differences():
-    """Differences of the forward call's own log probabilities and entropies, at logits around 300 and 2^24.  The level's
-    spacing (2^-15, 2) is a step that the logits take exactly."""
+    """Differences of the forward call's own log probabilities and entropies, at logits around 300 and -300 and in steps that
+    these take exactly."""
     rng = np.random.default_rng(4)
     n = 40
     say("bl_logprobs differences at a level")
